@@ -95,8 +95,10 @@ typedef enum {
     SS2D_ERR_CUDA = -8,   /* a CUDA call failed; see ss2d_last_error()       */
     SS2D_ERR_PTR = -9,    /* host and device pointers mixed in one call      */
     SS2D_ERR_VARIANT = -10, /* unknown kernel variant (ss2d_forward_ex)      */
-    SS2D_ERR_SCRATCH = -11  /* needs more scratch than ss2d_forward_noalloc's
+    SS2D_ERR_SCRATCH = -11, /* needs more scratch than ss2d_forward_noalloc's
                                fixed buffer holds                             */
+    SS2D_ERR_NORM = -12,    /* post or pre is not an ss2d_norm, or eps < 0    */
+    SS2D_ERR_STRIDE = -13   /* a stride is smaller than what it steps over    */
 } ss2d_status;
 
 typedef enum {
@@ -370,6 +372,61 @@ int selective_scan_fwd_front_timed(const void *x, const float *conv_w, const flo
 int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
                        const float *W_x, void *u, float *dt_raw, float *Bs, float *Cs,
                        int B, int D, int L, int N, int K, int dtype, void *stream);
+
+/* ---- block norms ---------------------------------------------------------
+ *
+ * The norm behind a mixer with its SiLU gate, the scaled sum into the
+ * residual stream, and the norm in front of the next block ("Vision Mamba ..."
+ * summary, section 4.3: a Vim block norms its input, gates the mixer's output
+ * by SiLU(z) and adds the residual; "VMamba" blocks norm the merged scan
+ * output before the gate), as one pass over rows of D values:
+ *   n  = N_post(x),  t = (n * w_post + b_post) * SiLU(z)
+ *   r' = r + s * t
+ *   y  = N_pre(r') * w_pre + b_pre
+ * with N_layer(x) = (x - mean) / sqrt(var + eps) (var the mean square about
+ * the mean), N_rms(x) = x / sqrt(mean(x^2) + eps).  Every part may be left out:
+ *   post = SS2D_NORM_NONE   n = x, w_post and b_post are not read
+ *   pre  = SS2D_NORM_NONE   no y (y, w_pre, b_pre are not read)
+ *   z, r, s, w_post, b_post, w_pre, b_pre NULL: no gate, r = 0, s = 1, w = 1, b = 0
+ * so post = rms with z alone is the gated output norm of a mixer's heads, and
+ * r, s with pre = layer alone the layer-scaled residual with the next norm.
+ *
+ * Layouts: x and z rows x D in dtype, row i at (i / group) * stride +
+ * (i % group) * D values, so that they may be slices of a wider projection
+ * (group = heads per token); stride >= group * D (SS2D_ERR_STRIDE).  r and r_out
+ * rows x D contiguous in r_dtype, which is dtype or SS2D_F32; y rows x D
+ * contiguous in dtype; s and the weights (D) float32.  D <= 8192, rows <= 2^40,
+ * group >= 1.  All pointers DEVICE pointers of the current device (SS2D_ERR_PTR
+ * otherwise), 16-byte aligned.  Asynchronous on `stream`.  r_out may be r;
+ * otherwise no output may overlap an input or another output.
+ * All arithmetic is float32 and every value is rounded once, on store: y is the
+ * norm of r' before its rounding to r_dtype. */
+typedef enum { SS2D_NORM_NONE = 0, SS2D_NORM_RMS = 1, SS2D_NORM_LAYER = 2 } ss2d_norm;
+
+int block_norm_fwd(const void *x, const void *z, const void *r, const float *s,
+                   const float *w_post, const float *b_post, const float *w_pre,
+                   const float *b_pre, void *r_out, void *y, long long rows, int D, int group,
+                   long long x_stride, long long z_stride, int post, int pre, float eps,
+                   int dtype, int r_dtype, void *stream);
+
+/* Backward of block_norm_fwd for the gradients dr_out (r_dtype; NULL = 0, only
+ * when there is a pre norm) of r' and dy (dtype; read when there is a pre
+ * norm) of y.  x, z, s and the weights are the forward's; r_out is r' as the
+ * forward stored it (read when there is a pre norm: the norm is
+ * differentiated at that value).  Writes dx, dz (dtype, contiguous; dz when z
+ * is given), dr (r_dtype; NULL = not wanted) and, where not NULL and where the
+ * call has the part, the float32 sums over the rows ds, dw_post, db_post,
+ * dw_pre, db_pre (D): each in a fixed order, the same bits on every call.
+ * With no rows the sums are zero.  dr may be dr_out, and dx may be x if x is
+ * contiguous; otherwise no output may overlap an input or another output.
+ * Scratch for the partial sums (5920 * D bytes at most) comes from the
+ * stream-ordered pool. */
+int block_norm_bwd(const void *x, const void *z, const void *r_out, const float *s,
+                   const float *w_post, const float *b_post, const float *w_pre,
+                   const void *dr_out, const void *dy, void *dx, void *dz, void *dr, float *ds,
+                   float *dw_post, float *db_post, float *dw_pre, float *db_pre,
+                   long long rows, int D, int group, long long x_stride, long long z_stride,
+                   int post, int pre, float eps, int dtype, int r_dtype, void *stream);
 
 /* Bounded waits.  The kernels that wait on an mbarrier (the front's
  * tensor-core completion) give up after a time limit instead of spinning

@@ -95,6 +95,12 @@ def lib() -> ctypes.CDLL:
             L.selective_scan_fwd_front_timed.restype = i
             L.ss2d_front_project.argtypes = [vp, fp, fp, fp, vp, fp, fp, fp] + [i] * 6 + [vp]
             L.ss2d_front_project.restype = i
+            ll = ctypes.c_longlong
+            norm = [ll, i, i, ll, ll, i, i, ctypes.c_float, i, i, vp]
+            L.block_norm_fwd.argtypes = [vp] * 10 + norm
+            L.block_norm_fwd.restype = i
+            L.block_norm_bwd.argtypes = [vp] * 17 + norm
+            L.block_norm_bwd.restype = i
             L.ss2d_check_waits.argtypes = []
             L.ss2d_check_waits.restype = i
             L.ss2d_wait_selftest.argtypes = [i, vp]
@@ -499,6 +505,133 @@ def ss2d_front_project(x, conv_w, conv_b, W_x, *, stream=None):
                                   _DTYPES[x.dtype], st)
     _check(rc)
     return u, dt_raw, Bs, Cs
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _norm_rows(t, like, name):
+    """(group, stride) of a tensor of rows: contiguous, or (M, G, D) / (M, D)
+    with contiguous groups of G rows at any stride (a slice of a projection)."""
+    if t.is_contiguous():
+        return None
+    D = t.shape[-1]
+    if t.dim() not in (2, 3) or t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != D) \
+            or t.stride(0) < t.shape[-2 if t.dim() == 3 else -1] * (D if t.dim() == 3 else 1):
+        raise ValueError(f"{name} must be contiguous, or (M, D) or (M, G, D) with packed rows")
+    return (t.shape[1] if t.dim() == 3 else 1), t.stride(0)
+
+
+def _norm_prepare(x, z, s, post, w_post, b_post, pre, w_pre, b_pre, rdt, what):
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    if post not in NORMS or pre not in NORMS:
+        raise ValueError("post and pre must be 'none', 'rms' or 'layer'")
+    if not x.is_cuda:
+        raise ValueError(f"{what} takes device tensors only")
+    if x.dim() < 1:
+        raise ValueError("x must have rows of at least one dimension")
+    if rdt not in (torch.float32, x.dtype):
+        raise TypeError("the residual must be float32 or of x's dtype")
+    D = x.shape[-1]
+    if z is not None and (z.dtype != x.dtype or z.shape != x.shape or z.device != x.device):
+        raise ValueError("z must have x's dtype, shape and device")
+    for n, t in (("s", s), ("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (D,) or
+                              t.device != x.device or not t.is_contiguous()):
+            raise ValueError(f"{n} must be a contiguous float32 tensor of shape {(D,)} on x's device")
+    lx = _norm_rows(x, x, "x")
+    lz = _norm_rows(z, x, "z") if z is not None else None
+    group = (lx or lz or (1, D))[0]
+    xs, zs = (lx or (0, group * D))[1], (lz or (0, group * D))[1]
+    rows = x.numel() // D if D else 0
+    return rows, D, group, xs, zs
+
+
+def _rows_like(t, x, dtype, name):
+    if t.dtype != dtype or t.shape != x.shape or t.device != x.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of x's shape and device")
+
+
+def _opt(t):
+    return _ptr(t) if t is not None else ctypes.c_void_p(0)
+
+
+def block_norm_fwd(x, *, z=None, r=None, s=None, post="none", w_post=None, b_post=None,
+                   pre="none", w_pre=None, b_pre=None, eps: float = 1e-5, r_out=None, y=None,
+                   stream=None):
+    """The norm behind a mixer, its gate, the scaled residual and the next
+    block's norm in one pass over rows of D values:
+
+      t = (N_post(x) * w_post + b_post) * SiLU(z);  r' = r + s * t;
+      y = N_pre(r') * w_pre + b_pre
+
+    post and pre: "none", "rms" or "layer".  x, z (..., D): contiguous, or
+    (M, D) / (M, G, D) slices with packed rows; r (..., D) float32 or of x's
+    dtype; s and the weights (D,) float32; each but x may be None.  Returns
+    (r', y), y None without a pre norm.  r_out may be r.  Device tensors only."""
+    rdt = r.dtype if r is not None else (r_out.dtype if r_out is not None else x.dtype)
+    rows, D, group, xs, zs = _norm_prepare(x, z, s, post, w_post, b_post, pre, w_pre, b_pre, rdt,
+                                           "block_norm_fwd")
+    if r is not None:
+        _rows_like(r, x, rdt, "r")
+    if r_out is None:
+        r_out = torch.empty(x.shape, dtype=rdt, device=x.device)
+    _rows_like(r_out, x, rdt, "r_out")
+    if pre == "none":
+        y = None
+    else:
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _rows_like(y, x, x.dtype, "y")
+    rc = lib().block_norm_fwd(_ptr(x), _opt(z), _opt(r), _opt(s), _opt(w_post), _opt(b_post),
+                              _opt(w_pre), _opt(b_pre), _ptr(r_out), _opt(y), rows, D, group, xs,
+                              zs, NORMS[post], NORMS[pre], float(eps), _DTYPES[x.dtype],
+                              _DTYPES[rdt], _stream(True, x.device, stream))
+    _check(rc)
+    return r_out, y
+
+
+NORM_GRAD_NAMES = ("dx", "dz", "dr", "ds", "dw_post", "db_post", "dw_pre", "db_pre")
+
+
+def block_norm_bwd(x, dr_out, dy=None, *, r_out=None, z=None, s=None, post="none", w_post=None,
+                   b_post=None, pre="none", w_pre=None, b_pre=None, eps: float = 1e-5,
+                   residual: bool = True, stream=None):
+    """Gradients of sum(dr_out * r') + sum(dy * y) of block_norm_fwd.
+
+    r_out: the r' that the forward returned (needed with a pre norm); dr_out
+    (its dtype; None = 0, with a pre norm only); dy of x's dtype (with a pre
+    norm).  Returns a dict: dx, dz of x's dtype, dr of r's (residual = False:
+    None), ds and the weights' gradients float32; None for what the call does
+    not have.  Device tensors only."""
+    rdt = dr_out.dtype if dr_out is not None else (r_out.dtype if r_out is not None else x.dtype)
+    rows, D, group, xs, zs = _norm_prepare(x, z, s, post, w_post, b_post, pre, w_pre, b_pre, rdt,
+                                           "block_norm_bwd")
+    has_pre = pre != "none"
+    if has_pre:
+        if r_out is None or dy is None:
+            raise ValueError("block_norm_bwd with a pre norm needs r_out and dy")
+        _rows_like(r_out, x, rdt, "r_out")
+        _rows_like(dy, x, x.dtype, "dy")
+    elif dr_out is None:
+        raise ValueError("block_norm_bwd without a pre norm needs dr_out")
+    if dr_out is not None:
+        _rows_like(dr_out, x, rdt, "dr_out")
+    new = lambda want, dt: torch.empty(x.shape, dtype=dt, device=x.device) if want else None  # noqa: E731
+    vec = lambda t: torch.empty((D,), dtype=torch.float32, device=x.device) if t is not None else None  # noqa: E731
+    has_post = post != "none"
+    g = dict(dx=new(True, x.dtype), dz=new(z is not None, x.dtype), dr=new(residual, rdt), ds=vec(s),
+             dw_post=vec(w_post) if has_post else None, db_post=vec(b_post) if has_post else None,
+             dw_pre=vec(w_pre) if has_pre else None, db_pre=vec(b_pre) if has_pre else None)
+    rc = lib().block_norm_bwd(_ptr(x), _opt(z), _opt(r_out) if has_pre else _opt(None), _opt(s),
+                              _opt(w_post), _opt(b_post), _opt(w_pre), _opt(dr_out),
+                              _opt(dy) if has_pre else _opt(None),
+                              *[_opt(g[n]) for n in NORM_GRAD_NAMES], rows, D, group, xs, zs,
+                              NORMS[post], NORMS[pre], float(eps), _DTYPES[x.dtype], _DTYPES[rdt],
+                              _stream(True, x.device, stream))
+    _check(rc)
+    return g
 
 
 def ss2d_check_waits() -> int:

@@ -848,6 +848,10 @@ const char *ss2d_status_string(int status)
     case SS2D_ERR_SCRATCH:
         return "problem needs more scratch than the fixed buffer of ss2d_forward_noalloc "
                "(SS2D_NOALLOC_SCRATCH_BYTES) holds";
+    case SS2D_ERR_NORM:
+        return "unknown norm (post, pre), or eps is negative";
+    case SS2D_ERR_STRIDE:
+        return "a stride is smaller than what it steps over";
     default:
         return "unknown status";
     }

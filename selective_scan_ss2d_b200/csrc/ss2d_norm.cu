@@ -1,0 +1,266 @@
+// ss2d_norm.cu -- the C ABI of the block norms (include/ss2d.h): argument
+// checks, thread layout and launches.
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include "ss2d.h"
+#include "ss2d_launch.h"
+#include "ss2d_norm.cuh"
+
+namespace {
+
+constexpr int kNormMaxD = 8192;
+
+struct NormCall {
+    ss2d::NormParams p;
+    int dtype, r_dtype;
+};
+
+int norm_validate(const NormCall &c)
+{
+    const ss2d::NormParams &p = c.p;
+    if (p.rows < 0 || p.D < 0 || p.D > kNormMaxD || p.group < 1 || p.rows > (1LL << 40))
+        return SS2D_ERR_SHAPE;
+    if (c.dtype != SS2D_F32 && c.dtype != SS2D_BF16 && c.dtype != SS2D_F16)
+        return SS2D_ERR_DTYPE;
+    if (c.r_dtype != SS2D_F32 && c.r_dtype != c.dtype)
+        return SS2D_ERR_DTYPE;
+    if (p.post < 0 || p.post > 2 || p.pre < 0 || p.pre > 2 || !(p.eps >= 0.f))
+        return SS2D_ERR_NORM;
+    const long long row = (long long)p.group * p.D;
+    if (p.xs < row || (p.z && p.zs < row))
+        return SS2D_ERR_STRIDE;
+    return SS2D_OK;
+}
+
+bool on_device(const void *q, int dev)
+{
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, q) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return (a.type == cudaMemoryTypeDevice && a.device == dev) || a.type == cudaMemoryTypeManaged;
+}
+
+int check(const void *const *need, int nneed, const void *const *opt, int nopt, const NormCall &c)
+{
+    for (int i = 0; i < nneed; ++i)
+        if (!need[i])
+            return SS2D_ERR_NULL;
+    for (int i = 0; i < nneed + nopt; ++i) {
+        const void *q = i < nneed ? need[i] : opt[i - nneed];
+        if (q && ((uintptr_t)q & 15u) != 0)
+            return SS2D_ERR_ALIGN;
+    }
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) {
+        ss2d::record_error("cudaGetDevice", e);
+        return SS2D_ERR_CUDA;
+    }
+    for (int i = 0; i < nneed + nopt; ++i) {
+        const void *q = i < nneed ? need[i] : opt[i - nneed];
+        if (q && !on_device(q, dev))
+            return SS2D_ERR_PTR;
+    }
+    return SS2D_OK;
+}
+
+// vectors of 16 bytes where every row of every tensor starts on a 16-byte
+// boundary, single values otherwise
+bool vector_rows(const NormCall &c)
+{
+    const int esz = c.dtype == SS2D_F32 ? 4 : 2;
+    return c.p.D % 8 == 0 && c.p.xs * esz % 16 == 0 && (!c.p.z || c.p.zs * esz % 16 == 0);
+}
+
+// Threads of a row's team: the smallest power of two that holds the row at E
+// values a thread.
+int team_size(int D, int E)
+{
+    int t = 1;
+    while (t * E < D)
+        t <<= 1;
+    return t;
+}
+
+template <typename Tin, typename Tr, int V, int E>
+cudaError_t launch(const NormCall &c, bool bwd, int grid, int threads, cudaStream_t st)
+{
+    if (bwd) {
+        const size_t smem = sizeof(float) * threads * E;
+        ss2d::norm_bwd_kernel<Tin, Tr, V, E><<<grid, threads, smem, st>>>(c.p);
+    } else {
+        ss2d::norm_fwd_kernel<Tin, Tr, V, E><<<grid, threads, 0, st>>>(c.p);
+    }
+    return cudaGetLastError();
+}
+
+template <typename Tin, typename Tr>
+cudaError_t launch_type(const NormCall &c, bool bwd, int grid, int threads, bool vec, cudaStream_t st)
+{
+    constexpr int V = 8;   // one 16-byte vector of 16-bit values, two of float32
+    if (c.p.D <= 4096)
+        return vec ? launch<Tin, Tr, V, 8>(c, bwd, grid, threads, st)
+                   : launch<Tin, Tr, 1, 8>(c, bwd, grid, threads, st);
+    return vec ? launch<Tin, Tr, V, 16>(c, bwd, grid, threads, st)
+               : launch<Tin, Tr, 1, 16>(c, bwd, grid, threads, st);
+}
+
+cudaError_t launch_norm(const NormCall &c, bool bwd, int grid, int threads, cudaStream_t st)
+{
+    const bool vec = vector_rows(c);
+    const bool rf = c.r_dtype == SS2D_F32;
+    switch (c.dtype) {
+    case SS2D_F32:
+        return launch_type<float, float>(c, bwd, grid, threads, vec, st);
+    case SS2D_BF16:
+        return rf ? launch_type<__nv_bfloat16, float>(c, bwd, grid, threads, vec, st)
+                  : launch_type<__nv_bfloat16, __nv_bfloat16>(c, bwd, grid, threads, vec, st);
+    default:
+        return rf ? launch_type<__half, float>(c, bwd, grid, threads, vec, st)
+                  : launch_type<__half, __half>(c, bwd, grid, threads, vec, st);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int block_norm_fwd(const void *x, const void *z, const void *r, const float *s, const float *w_post,
+                   const float *b_post, const float *w_pre, const float *b_pre, void *r_out, void *y,
+                   long long rows, int D, int group, long long x_stride, long long z_stride, int post, int pre,
+                   float eps, int dtype, int r_dtype, void *stream)
+{
+    NormCall c{};
+    c.dtype = dtype;
+    c.r_dtype = r_dtype;
+    ss2d::NormParams &p = c.p;
+    p.x = x;
+    p.z = z;
+    p.r = r;
+    p.s = s;
+    p.w_post = w_post;
+    p.b_post = b_post;
+    p.w_pre = w_pre;
+    p.b_pre = b_pre;
+    p.r_out = r_out;
+    p.y = y;
+    p.rows = rows;
+    p.D = D;
+    p.group = group;
+    p.xs = x_stride;
+    p.zs = z_stride;
+    p.post = post;
+    p.pre = pre;
+    p.eps = eps;
+    int rc = norm_validate(c);
+    if (rc != SS2D_OK || rows == 0 || D == 0)
+        return rc;
+    const void *need[] = {x, r_out, pre ? y : x};
+    const void *opt[] = {z, r, s, w_post, b_post, w_pre, b_pre};
+    rc = check(need, 3, opt, 7, c);
+    if (rc != SS2D_OK)
+        return rc;
+    p.tpr = team_size(D, D <= 4096 ? 8 : 16);
+    const int threads = p.tpr > 256 ? p.tpr : 256;
+    const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
+    const int grid = ctas > (1 << 30) ? 1 << 30 : (int)ctas;
+    const cudaError_t e = launch_norm(c, false, grid, threads, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        ss2d::record_error("kernel launch", e);
+        return SS2D_ERR_CUDA;
+    }
+    return SS2D_OK;
+}
+
+int block_norm_bwd(const void *x, const void *z, const void *r_out, const float *s, const float *w_post,
+                   const float *b_post, const float *w_pre, const void *dr_out, const void *dy, void *dx, void *dz,
+                   void *dr, float *ds, float *dw_post, float *db_post, float *dw_pre, float *db_pre,
+                   long long rows, int D, int group, long long x_stride, long long z_stride, int post, int pre,
+                   float eps, int dtype, int r_dtype, void *stream)
+{
+    NormCall c{};
+    c.dtype = dtype;
+    c.r_dtype = r_dtype;
+    ss2d::NormParams &p = c.p;
+    p.x = x;
+    p.z = z;
+    p.r = r_out;
+    p.s = s;
+    p.w_post = w_post;
+    p.b_post = b_post;
+    p.w_pre = w_pre;
+    p.dr_out = dr_out;
+    p.dy = dy;
+    p.dx = dx;
+    p.dz = dz;
+    p.dr = dr;
+    p.rows = rows;
+    p.D = D;
+    p.group = group;
+    p.xs = x_stride;
+    p.zs = z_stride;
+    p.post = post;
+    p.pre = pre;
+    p.eps = eps;
+    int rc = norm_validate(c);
+    if (rc != SS2D_OK || D == 0)
+        return rc;
+    // column sums of a part that the call does not have are not written
+    const ss2d::NormSums out{{ds, post ? dw_post : nullptr, post ? db_post : nullptr, pre ? dw_pre : nullptr,
+                              pre ? db_pre : nullptr}};
+    for (int i = 0; i < ss2d::kNormCols; ++i)
+        p.cols |= (out.out[i] ? 1 : 0) << i;
+    const void *sums[] = {out.out[0], out.out[1], out.out[2], out.out[3], out.out[4]};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (rows == 0) {
+        rc = check(nullptr, 0, sums, 5, c);
+        for (int i = 0; i < ss2d::kNormCols && rc == SS2D_OK && e == cudaSuccess; ++i)
+            if (out.out[i])
+                e = cudaMemsetAsync(out.out[i], 0, sizeof(float) * D, st);
+        if (rc == SS2D_OK && e != cudaSuccess) {
+            ss2d::record_error("cudaMemsetAsync", e);
+            return SS2D_ERR_CUDA;
+        }
+        return rc;
+    }
+    const void *need[] = {x, dx, pre ? r_out : x, pre ? dy : x, pre ? x : dr_out, z ? dz : x};
+    const void *opt[] = {z, s, w_post, b_post, w_pre, dr_out, dr, ds, dw_post, db_post, dw_pre, db_pre};
+    rc = check(need, 6, opt, 12, c);
+    if (rc != SS2D_OK)
+        return rc;
+    if (!z)
+        p.dz = nullptr;
+    const int E = D <= 4096 ? 8 : 16;
+    p.tpr = team_size(D, E);
+    const int threads = p.tpr > 256 ? p.tpr : 256;
+    const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
+    // two CTAs of 256 threads at the kernel's registers fill an SM; more CTAs only add partials
+    const int grid = ctas > 148 * 2 ? 148 * 2 : (int)ctas;
+    void *part = nullptr;
+    if (p.cols) {
+        rc = ss2d::scratch_alloc(&part, sizeof(float) * ss2d::kNormCols * grid * (size_t)D, st);
+        if (rc != SS2D_OK)
+            return rc;
+    }
+    p.part = static_cast<float *>(part);
+    e = launch_norm(c, true, grid, threads, st);
+    if (e == cudaSuccess && p.cols) {
+        ss2d::norm_colsum_kernel<<<dim3((D + 31) / 32, ss2d::kNormCols), 256, 0, st>>>(p.part, out, grid, D);
+        e = cudaGetLastError();
+    }
+    cudaError_t ef = cudaSuccess;
+    if (part)
+        ef = cudaFreeAsync(part, st);
+    if (e != cudaSuccess || ef != cudaSuccess) {
+        ss2d::record_error(e != cudaSuccess ? "kernel launch" : "cudaFreeAsync", e != cudaSuccess ? e : ef);
+        return SS2D_ERR_CUDA;
+    }
+    return SS2D_OK;
+}
+
+}  // extern "C"
