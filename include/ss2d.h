@@ -98,7 +98,9 @@ typedef enum {
     SS2D_ERR_SCRATCH = -11, /* needs more scratch than ss2d_forward_noalloc's
                                fixed buffer holds                             */
     SS2D_ERR_NORM = -12,    /* post or pre is not an ss2d_norm, or eps < 0    */
-    SS2D_ERR_STRIDE = -13   /* a stride is smaller than what it steps over    */
+    SS2D_ERR_STRIDE = -13,  /* a stride is smaller than what it steps over    */
+    SS2D_ERR_HEADS = -14    /* H is no multiple of HK, or a head size is not
+                               supported (gated delta rule)                   */
 } ss2d_status;
 
 typedef enum {
@@ -372,6 +374,83 @@ int selective_scan_fwd_front_timed(const void *x, const float *conv_w, const flo
 int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
                        const float *W_x, void *u, float *dt_raw, float *Bs, float *Cs,
                        int B, int D, int L, int N, int K, int dtype, void *stream);
+
+/* ---- gated delta rule ------------------------------------------------------
+ *
+ * A linear recurrence like the selective scan, with a matrix for a state and
+ * an update that replaces what the state holds for a key instead of only adding
+ * to it.  Per sequence and value head h (key head h / (H / HK)), S_0 = h0 or 0:
+ *   d_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t)
+ *   S_t = exp(g_t) S_{t-1} + k_t d_t^T            S (DK, DV)
+ *   o_t = scale * S_t^T q_t
+ * so that without decay (g = 0), with |k| = 1 and beta = 1, S_t^T k_t = v_t.
+ * Keys are normally scaled to |k| <= 1 by the caller and g <= 0, 0 <= beta <= 1;
+ * the recurrence is computed as written for any values (it grows where it grows).
+ * g = -infinity forgets the state; below -200 exp(g) is 0 in float32 and g is read
+ * as -200.
+ *
+ * Layouts.  A token's row holds its heads: q, k rows of HK x DK, v rows of H x DV
+ * in dtype, token t at t * stride values (so q, k and v may be slices of one
+ * projection; stride >= the row, SS2D_ERR_STRIDE; stride * sizeof(dtype) a multiple
+ * of 16).  g, beta (tokens, H) float32, o (tokens, H, DV) dtype, h0 and h_last
+ * (nseq, H, DK, DV) float32, all contiguous.  H a multiple of HK; DK a multiple of
+ * 16 in 16..128, DV a multiple of 16 in 16..256 (SS2D_ERR_HEADS); H <= 65535.
+ * Sequences:
+ *   cu_seqlens NULL   nseq sequences of L tokens, token b * L + t
+ *   cu_seqlens        int32 device array of nseq + 1 ascending token positions in
+ *                     0..L: sequence n is the tokens cu[n] .. cu[n + 1] - 1, possibly
+ *                     none, of L tokens in all.  The array is read on the device:
+ *                     positions outside 0..L are moved inside, and if they do
+ *                     not ascend the outputs are unspecified (no access leaves
+ *                     the buffers).  Tokens in no sequence are not read, and their
+ *                     rows of the outputs are left as they were.
+ * reverse != 0: every sequence is read from its last token to its first (direction
+ * 1 of a bidirectional block), outputs in token order.  h0 NULL = zeros; h_last
+ * NULL = not wanted; h_last may be h0, otherwise no output may overlap an input.  A
+ * sequence of no tokens gets h_last = h0.
+ * All pointers DEVICE pointers of the current device (SS2D_ERR_PTR otherwise),
+ * 16-byte aligned.  Asynchronous on `stream`; scratch (per 64 tokens and head 24 to
+ * 50 KB) comes from the stream-ordered pool.
+ *
+ * Precision: the state and all arithmetic are float32 (products on the tensor
+ * cores of operands split into bfloat16 parts that hold them to float32 accuracy);
+ * o is rounded once, on store.  Where o is 16 bits and no h_last is asked for,
+ * intermediate values keep 16 bits of mantissa.  A value that is not finite
+ * reaches every output of its sequence from its group of 64 tokens on. */
+int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const float *g,
+                         const float *beta, const float *h0, void *o, float *h_last,
+                         const int *cu_seqlens, int nseq, int L, int HK, int H, int DK, int DV,
+                         long long q_stride, long long k_stride, long long v_stride,
+                         float scale, int reverse, int dtype, void *stream);
+
+/* Backward of gated_delta_rule_fwd: the gradients of sum(dout * o) +
+ * sum(dh_last * h_last).  dout (tokens, H, DV) dtype, dh_last (nseq, H, DK, DV)
+ * float32 or NULL (0).  Writes dq, dk (tokens, HK, DK) and dv (tokens, H, DV) in dtype,
+ * contiguous, the gradients of shared key heads summed over their value heads in
+ * a fixed order; dg, dbeta (tokens, H) float32; dh0 (nseq, H, DK, DV) float32 or NULL
+ * (not wanted; may be dh_last).  The forward's other arguments and rules hold.
+ * The states are computed again from the inputs and kept in scratch: per 64 tokens
+ * and head 8 * DKP * DV + 784 * DV + 49920 bytes (DKP = 64 or 128, DK rounded up), from
+ * the stream-ordered pool.  No atomics: the same bits on every call. */
+int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const float *g,
+                         const float *beta, const float *h0, const void *dout,
+                         const float *dh_last, void *dq, void *dk, void *dv, float *dg,
+                         float *dbeta, float *dh0, const int *cu_seqlens, int nseq, int L,
+                         int HK, int H, int DK, int DV, long long q_stride, long long k_stride,
+                         long long v_stride, float scale, int reverse, int dtype, void *stream);
+
+/* One token of B sequences (the recurrent form, for serving): row b updates state
+ * slots[b] of the pool `state` (nstates, H, DK, DV) float32 in place (slots NULL:
+ * state b; then nstates >= B, SS2D_ERR_SHAPE otherwise) and writes o (B, H, DV).  q, k
+ * (B, HK, DK) and v (B, H, DV) in dtype at their strides, g, beta (B, H) float32.  slots is
+ * an int32 device array: a row whose slot is outside 0..nstates - 1 (-1: padding)
+ * is skipped, and so is every row but the first of those that name the same slot;
+ * a skipped row's o is zero.  No scratch; other rules as above. */
+int gated_delta_rule_step(const void *q, const void *k, const void *v, const float *g,
+                          const float *beta, float *state, const int *slots, void *o, int B,
+                          long long nstates, int HK, int H, int DK, int DV, long long q_stride,
+                          long long k_stride, long long v_stride, float scale, int dtype,
+                          void *stream);
 
 /* ---- block norms ---------------------------------------------------------
  *

@@ -101,6 +101,13 @@ def lib() -> ctypes.CDLL:
             L.block_norm_fwd.restype = i
             L.block_norm_bwd.argtypes = [vp] * 17 + norm
             L.block_norm_bwd.restype = i
+            heads = [i, i, i, i, ll, ll, ll, ctypes.c_float]   # HK, H, DK, DV, strides, scale
+            L.gated_delta_rule_fwd.argtypes = [vp] * 9 + [i, i] + heads + [i, i, vp]
+            L.gated_delta_rule_fwd.restype = i
+            L.gated_delta_rule_bwd.argtypes = [vp] * 15 + [i, i] + heads + [i, i, vp]
+            L.gated_delta_rule_bwd.restype = i
+            L.gated_delta_rule_step.argtypes = [vp] * 8 + [i, ll] + heads + [i, vp]
+            L.gated_delta_rule_step.restype = i
             L.ss2d_check_waits.argtypes = []
             L.ss2d_check_waits.restype = i
             L.ss2d_wait_selftest.argtypes = [i, vp]
@@ -505,6 +512,162 @@ def ss2d_front_project(x, conv_w, conv_b, W_x, *, stream=None):
                                   _DTYPES[x.dtype], st)
     _check(rc)
     return u, dt_raw, Bs, Cs
+
+
+def _token_stride(t, name):
+    """Values between tokens of (..., tokens, heads, size): packed heads, tokens at
+    any stride (slices of one projection), batches of whole token runs."""
+    if t.numel() == 0 or t.is_contiguous():
+        return t.shape[-2] * t.shape[-1]
+    st, sh = t.stride(), t.shape
+    ok = (st[-1] == 1 or sh[-1] == 1) and (st[-2] == sh[-1] or sh[-2] == 1)
+    row = st[-3] if sh[-3] > 1 else (st[0] if t.dim() == 4 else sh[-2] * sh[-1])
+    if t.dim() == 4 and sh[0] > 1 and sh[1] > 1:
+        ok = ok and st[0] == sh[1] * st[1]
+    if not ok or row < sh[-2] * sh[-1]:
+        raise ValueError(f"{name} must have packed heads and one stride between tokens")
+    return row
+
+
+def _delta_prepare(q, k, v, g, beta, what):
+    """Checks shared by the gated delta rule's calls; (HK, H, DK, DV), strides, dtype."""
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"q must be float32, bfloat16 or float16, got {q.dtype}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must share one dtype")
+    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+        raise TypeError("g and beta must be float32")
+    HK, DK = q.shape[-2:]
+    H, DV = v.shape[-2:]
+    lead = tuple(q.shape[:-2])
+    if tuple(k.shape) != tuple(q.shape) or tuple(v.shape[:-2]) != lead or \
+            tuple(g.shape) != lead + (H,) or tuple(beta.shape) != lead + (H,):
+        raise ValueError(f"inconsistent shapes for {what}")
+    for t in (q, k, v, g, beta):
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{what} takes device tensors only, on one device")
+    if not g.is_contiguous() or not beta.is_contiguous():
+        raise ValueError("g and beta must be contiguous")
+    strides = [_token_stride(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    return (HK, H, DK, DV), strides, _DTYPES[q.dtype]
+
+
+def _delta_sequences(q, cu_seqlens, what):
+    """(nseq, L) of a call on (B, L, ...) tensors."""
+    B, L = q.shape[:2]
+    if cu_seqlens is None:
+        return B, L
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
+            cu_seqlens.device != q.device or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 vector on the inputs' device")
+    if B != 1:
+        raise ValueError(f"{what} with cu_seqlens takes one batch element of packed tokens")
+    return cu_seqlens.numel() - 1, L
+
+
+def _like(t, shape, dtype, device, name):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=None,
+                         reverse: bool = False, final_state: bool = False, o=None, h_last=None,
+                         stream=None):
+    """Gated delta rule over whole sequences:
+
+      S_t = exp(g_t) S_{t-1} + k_t d_t^T,  d_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),
+      o_t = scale S_t^T q_t
+
+    q, k (B, L, HK, DK), v (B, L, H, DV) of one dtype, heads packed and tokens at
+    any stride; g, beta (B, L, H) float32; h0 (sequences, H, DK, DV) float32.
+    cu_seqlens (int32, device): B = 1 and the tokens of several sequences packed;
+    tokens in none of them leave o as it was.  scale defaults to DK ** -0.5; reverse
+    reads every sequence from its end.  Returns (o, h_last): o (B, L, H, DV) of
+    q's dtype, h_last like h0, None unless final_state or h_last is given (it may
+    be h0).  Device tensors only."""
+    dims, strides, dt = _delta_prepare(q, k, v, g, beta, "gated_delta_rule_fwd")
+    if q.dim() != 4:
+        raise ValueError("q must be (B, L, HK, DK)")
+    nseq, L = _delta_sequences(q, cu_seqlens, "gated_delta_rule_fwd")
+    HK, H, DK, DV = dims
+    sdims = (nseq, H, DK, DV)
+    if h0 is not None:
+        _like(h0, sdims, torch.float32, q.device, "h0")
+    if o is None:
+        o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+    _like(o, v.shape, q.dtype, q.device, "o")
+    if h_last is None and final_state:
+        h_last = torch.empty(sdims, dtype=torch.float32, device=q.device)
+    if h_last is not None:
+        _like(h_last, sdims, torch.float32, q.device, "h_last")
+    rc = lib().gated_delta_rule_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _opt(h0), _ptr(o),
+                                    _opt(h_last), _opt(cu_seqlens), nseq, L, *dims, *strides,
+                                    DK ** -0.5 if scale is None else float(scale), int(reverse), dt,
+                                    _stream(True, q.device, stream))
+    _check(rc)
+    return o, h_last
+
+
+DELTA_GRAD_NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dh0")
+
+
+def gated_delta_rule_bwd(q, k, v, g, beta, do, h0=None, dh_last=None, *, scale=None,
+                         cu_seqlens=None, reverse: bool = False, stream=None):
+    """Gradients of sum(do * o) + sum(dh_last * h_last) of gated_delta_rule_fwd.
+    do (B, L, H, DV) of q's dtype; dh_last (sequences, H, DK, DV) float32 or None.
+    Returns a dict: dq, dk, dv of q's dtype, dg, dbeta float32, dh0 float32 (None
+    without h0).  Rows of tokens in no sequence are zero.  Device tensors only."""
+    dims, strides, dt = _delta_prepare(q, k, v, g, beta, "gated_delta_rule_bwd")
+    if q.dim() != 4:
+        raise ValueError("q must be (B, L, HK, DK)")
+    nseq, L = _delta_sequences(q, cu_seqlens, "gated_delta_rule_bwd")
+    HK, H, DK, DV = dims
+    sdims = (nseq, H, DK, DV)
+    _like(do, v.shape, q.dtype, q.device, "do")
+    for t, n in ((h0, "h0"), (dh_last, "dh_last")):
+        if t is not None:
+            _like(t, sdims, torch.float32, q.device, n)
+    # packed tokens may leave rows that belong to no sequence: their gradient is zero
+    new = torch.empty if cu_seqlens is None else torch.zeros
+    gr = dict(dq=new(q.shape, dtype=q.dtype, device=q.device),
+              dk=new(q.shape, dtype=q.dtype, device=q.device),
+              dv=new(v.shape, dtype=q.dtype, device=q.device),
+              dg=new(g.shape, dtype=torch.float32, device=q.device),
+              dbeta=new(g.shape, dtype=torch.float32, device=q.device),
+              dh0=torch.empty(sdims, dtype=torch.float32, device=q.device) if h0 is not None else None)
+    rc = lib().gated_delta_rule_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _opt(h0), _ptr(do),
+                                    _opt(dh_last), *[_opt(gr[n]) for n in DELTA_GRAD_NAMES],
+                                    _opt(cu_seqlens), nseq, L, *dims, *strides,
+                                    DK ** -0.5 if scale is None else float(scale), int(reverse), dt,
+                                    _stream(True, q.device, stream))
+    _check(rc)
+    return gr
+
+
+def gated_delta_rule_step(q, k, v, g, beta, state, slots=None, *, scale=None, o=None, stream=None):
+    """One token of B sequences, the states updated in place: q, k (B, HK, DK), v
+    (B, H, DV), g, beta (B, H) float32; state (states, H, DK, DV) float32; slots (B,)
+    int32 on the device: the state of each row (None: row b has state b).  A row
+    whose slot is outside the pool, or named by an earlier row, is skipped and
+    its output zero.  Returns o (B, H, DV) of q's dtype.  Device tensors only."""
+    dims, strides, dt = _delta_prepare(q, k, v, g, beta, "gated_delta_rule_step")
+    if q.dim() != 3:
+        raise ValueError("q must be (B, HK, DK)")
+    B, (HK, H, DK, DV) = q.shape[0], dims
+    if state.dim() != 4:
+        raise ValueError("state must be (states, H, DK, DV)")
+    _like(state, (state.shape[0], H, DK, DV), torch.float32, q.device, "state")
+    if slots is not None:
+        _like(slots, (B,), torch.int32, q.device, "slots")
+    if o is None:
+        o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+    _like(o, v.shape, q.dtype, q.device, "o")
+    rc = lib().gated_delta_rule_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
+                                     _opt(slots), _ptr(o), B, state.shape[0], *dims, *strides,
+                                     DK ** -0.5 if scale is None else float(scale), dt,
+                                     _stream(True, q.device, stream))
+    _check(rc)
+    return o
 
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}

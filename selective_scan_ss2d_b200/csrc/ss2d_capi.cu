@@ -852,6 +852,8 @@ const char *ss2d_status_string(int status)
         return "unknown norm (post, pre), or eps is negative";
     case SS2D_ERR_STRIDE:
         return "a stride is smaller than what it steps over";
+    case SS2D_ERR_HEADS:
+        return "H must be a multiple of HK, DK a multiple of 16 in 16..128, DV one in 16..256";
     default:
         return "unknown status";
     }

@@ -1,0 +1,302 @@
+// ss2d_delta.cu -- the C ABI of the gated delta rule (include/ss2d.h):
+// argument checks, scratch and the choice between the token-by-token kernel
+// and the chunked ones.
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include "ss2d.h"
+#include "ss2d_delta_launch.h"
+#include "ss2d_launch.h"
+
+namespace {
+
+using ss2d::DeltaParams;
+using ss2d::DeltaPlan;
+using ss2d::kDeltaC;
+
+// Calls whose sequences are known to be this short go token by token.
+constexpr int kRecurLen = 4;
+
+struct Call {
+    DeltaParams p;
+    int dtype;
+    cudaStream_t st;
+};
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+int validate(const Call &c)
+{
+    const DeltaParams &p = c.p;
+    if (p.nseq < 0 || p.L < 0 || p.HK < 0 || p.H < 0 || p.H > 65535)
+        return SS2D_ERR_SHAPE;
+    if (c.dtype != SS2D_F32 && c.dtype != SS2D_BF16 && c.dtype != SS2D_F16)
+        return SS2D_ERR_DTYPE;
+    if ((p.HK == 0 ? p.H != 0 : p.H % p.HK != 0) || p.DK < 16 || p.DK > ss2d::kDeltaMaxDK || p.DK % 16 != 0 ||
+        p.DV < 16 || p.DV > ss2d::kDeltaMaxDV || p.DV % 16 != 0)
+        return SS2D_ERR_HEADS;
+    if (p.qs < (long long)p.HK * p.DK || p.ks < (long long)p.HK * p.DK || p.vs < (long long)p.H * p.DV)
+        return SS2D_ERR_STRIDE;
+    return SS2D_OK;
+}
+
+// every pointer of `need` is given; those and `opt` are aligned device memory; token strides keep rows aligned
+int check(const Call &c, const void *const *need, int nneed, const void *const *opt, int nopt)
+{
+    const int esz = c.dtype == SS2D_F32 ? 4 : 2;
+    for (int i = 0; i < nneed; ++i)
+        if (!need[i])
+            return SS2D_ERR_NULL;
+    for (int i = 0; i < nneed + nopt; ++i)
+        if (((uintptr_t)(i < nneed ? need[i] : opt[i - nneed]) & 15u) != 0)
+            return SS2D_ERR_ALIGN;
+    if (c.p.qs * esz % 16 != 0 || c.p.ks * esz % 16 != 0 || c.p.vs * esz % 16 != 0)
+        return SS2D_ERR_ALIGN;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) {
+        ss2d::record_error("cudaGetDevice", e);
+        return SS2D_ERR_CUDA;
+    }
+    for (int i = 0; i < nneed + nopt; ++i) {
+        const void *q = i < nneed ? need[i] : opt[i - nneed];
+        if (!q)
+            continue;
+        cudaPointerAttributes a;
+        e = cudaPointerGetAttributes(&a, q);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return SS2D_ERR_PTR;
+        }
+        if (!(a.type == cudaMemoryTypeDevice && a.device == dev) && a.type != cudaMemoryTypeManaged)
+            return SS2D_ERR_PTR;
+    }
+    return SS2D_OK;
+}
+
+int run(Call &c, const DeltaPlan &pl, int what)
+{
+    cudaError_t e;
+    switch (c.dtype) {
+    case SS2D_BF16:
+        e = ss2d::launch_delta_bf16(c.p, pl, what, c.st);
+        break;
+    case SS2D_F16:
+        e = ss2d::launch_delta_f16(c.p, pl, what, c.st);
+        break;
+    default:
+        e = ss2d::launch_delta_f32(c.p, pl, what, c.st);
+        break;
+    }
+    if (e != cudaSuccess) {
+        ss2d::record_error("kernel launch", e);
+        return SS2D_ERR_CUDA;
+    }
+    return SS2D_OK;
+}
+
+// the chunked passes, with their scratch
+int run_chunked(Call &c, bool bwd)
+{
+    DeltaParams &p = c.p;
+    DeltaPlan pl;
+    pl.dkp = p.DK <= 64 ? 64 : 128;
+    pl.npi = c.dtype == SS2D_F32 ? 3 : c.dtype == SS2D_F16 ? 2 : 1;
+    pl.np = bwd || p.h_last || c.dtype == SS2D_F32 ? 3 : 2;
+    pl.npp = bwd || c.dtype == SS2D_F32 ? 3 : 2;
+    p.NC = (p.L + kDeltaC - 1) / kDeltaC;
+    p.nslots = p.cu ? p.T / kDeltaC + p.nseq : (long long)p.nseq * p.NC;
+    if (p.nslots > INT_MAX || p.HK > 65535)
+        return SS2D_ERR_SHAPE;
+    const size_t n = (size_t)p.nslots, nh = n * p.H, part = (size_t)kDeltaC * kDeltaC * 2;
+    const size_t kp = pl.npi > 1 ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
+    const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
+    const size_t kl = bwd ? nh * (p.DV / 16) * kDeltaC * 4 : 0;
+    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx, vx, kl};
+    size_t off[11], total = 0;
+    for (int i = 0; i < 11; ++i) {
+        off[i] = total;
+        total += up256(size[i]);
+    }
+    void *scratch = nullptr;
+    int rc = ss2d::scratch_alloc(&scratch, total, c.st);
+    if (rc != SS2D_OK)
+        return rc;
+    char *b = static_cast<char *>(scratch);
+    auto f = [&](int i) { return reinterpret_cast<float *>(b + off[i]); };
+    p.kp = b + off[0];
+    p.qp = b + off[1];
+    p.Tp = b + off[2];
+    p.Pp = b + off[3];
+    p.vec = f(4);
+    p.Sx = f(5);
+    p.dSx = f(6);
+    p.Vx = f(7);
+    p.Yx = f(8);
+    p.dXx = f(9);
+    p.klx = f(10);
+    rc = run(c, pl, bwd ? ss2d::kDeltaBwd : ss2d::kDeltaFwd);
+    const cudaError_t e = cudaFreeAsync(scratch, c.st);
+    if (rc == SS2D_OK && e != cudaSuccess) {
+        ss2d::record_error("cudaFreeAsync", e);
+        return SS2D_ERR_CUDA;
+    }
+    return rc;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                         const float *h0, void *o, float *h_last, const int *cu_seqlens, int nseq, int L, int HK,
+                         int H, int DK, int DV, long long q_stride, long long k_stride, long long v_stride,
+                         float scale, int reverse, int dtype, void *stream)
+{
+    Call c{};
+    DeltaParams &p = c.p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    p.h0 = h0;
+    p.o = o;
+    p.h_last = h_last;
+    p.cu = cu_seqlens;
+    p.nseq = nseq;
+    p.L = L;
+    p.HK = HK;
+    p.H = H;
+    p.DK = DK;
+    p.DV = DV;
+    p.qs = q_stride;
+    p.ks = k_stride;
+    p.vs = v_stride;
+    p.scale = scale;
+    p.reverse = reverse ? 1 : 0;
+    p.T = cu_seqlens ? L : (long long)nseq * L;
+    c.dtype = dtype;
+    c.st = static_cast<cudaStream_t>(stream);
+    int rc = validate(c);
+    if (rc != SS2D_OK || nseq == 0 || H == 0 || (p.T == 0 && !h_last))
+        return rc;
+    const void *opt[] = {h0, h_last, cu_seqlens, q, k, v, g, beta, o};
+    const void *need[] = {q, k, v, g, beta, o};
+    rc = p.T ? check(c, need, 6, opt, 3) : check(c, nullptr, 0, opt, 3);
+    if (rc != SS2D_OK)
+        return rc;
+    if (L <= kRecurLen)
+        return run(c, DeltaPlan{}, ss2d::kDeltaRecur);
+    return run_chunked(c, false);
+}
+
+int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                         const float *h0, const void *dout, const float *dh_last, void *dq, void *dk, void *dv,
+                         float *dg, float *dbeta, float *dh0, const int *cu_seqlens, int nseq, int L, int HK, int H,
+                         int DK, int DV, long long q_stride, long long k_stride, long long v_stride, float scale,
+                         int reverse, int dtype, void *stream)
+{
+    Call c{};
+    DeltaParams &p = c.p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    p.h0 = h0;
+    p.dout = dout;
+    p.dh_last = dh_last;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dg = dg;
+    p.dbeta = dbeta;
+    p.dh0 = dh0;
+    p.cu = cu_seqlens;
+    p.nseq = nseq;
+    p.L = L;
+    p.HK = HK;
+    p.H = H;
+    p.DK = DK;
+    p.DV = DV;
+    p.qs = q_stride;
+    p.ks = k_stride;
+    p.vs = v_stride;
+    p.scale = scale;
+    p.reverse = reverse ? 1 : 0;
+    p.T = cu_seqlens ? L : (long long)nseq * L;
+    c.dtype = dtype;
+    c.st = static_cast<cudaStream_t>(stream);
+    int rc = validate(c);
+    if (rc != SS2D_OK || nseq == 0 || H == 0 || (p.T == 0 && !dh0))
+        return rc;
+    const void *opt[] = {h0, dh_last, dh0, cu_seqlens};
+    const void *need[] = {q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
+    rc = p.T ? check(c, need, 11, opt, 4) : check(c, nullptr, 0, opt, 4);
+    if (rc != SS2D_OK)
+        return rc;
+    if (p.T == 0) {   // no token anywhere: the state passes through
+        const size_t bytes = (size_t)nseq * H * DK * DV * 4;
+        cudaError_t e = cudaSuccess;
+        if (!dh_last)
+            e = cudaMemsetAsync(dh0, 0, bytes, c.st);
+        else if (dh0 != dh_last)
+            e = cudaMemcpyAsync(dh0, dh_last, bytes, cudaMemcpyDeviceToDevice, c.st);
+        if (e != cudaSuccess) {
+            ss2d::record_error("cudaMemcpyAsync", e);
+            return SS2D_ERR_CUDA;
+        }
+        return SS2D_OK;
+    }
+    return run_chunked(c, true);
+}
+
+int gated_delta_rule_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                          float *state, const int *slots, void *o, int B, long long nstates, int HK, int H, int DK,
+                          int DV, long long q_stride, long long k_stride, long long v_stride, float scale, int dtype,
+                          void *stream)
+{
+    Call c{};
+    DeltaParams &p = c.p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    p.o = o;
+    p.pool = state;
+    p.slots = slots;
+    p.npool = nstates;
+    p.nseq = B;
+    p.L = 1;
+    p.HK = HK;
+    p.H = H;
+    p.DK = DK;
+    p.DV = DV;
+    p.qs = q_stride;
+    p.ks = k_stride;
+    p.vs = v_stride;
+    p.scale = scale;
+    p.T = B;
+    c.dtype = dtype;
+    c.st = static_cast<cudaStream_t>(stream);
+    int rc = validate(c);
+    if (rc != SS2D_OK)
+        return rc;
+    if (nstates < 0 || (!slots && nstates < B))
+        return SS2D_ERR_SHAPE;
+    if (B == 0 || H == 0)
+        return SS2D_OK;
+    // a pool of no states: every slot is skipped, the pointer is not read
+    const void *need[] = {q, k, v, g, beta, o, nstates ? state : o};
+    rc = check(c, need, 7, reinterpret_cast<const void *const *>(&slots), 1);
+    if (rc != SS2D_OK)
+        return rc;
+    if (!p.pool)
+        p.pool = static_cast<float *>(o);
+    return run(c, DeltaPlan{}, ss2d::kDeltaRecur);
+}
+
+}  // extern "C"

@@ -1,0 +1,632 @@
+// ss2d_delta.cuh -- the gated delta rule: what its kernels share, the
+// token-by-token kernel, and the kernel that prepares the chunks.
+//
+// Per sequence and value head, state S (DK, DV), S_0 = h0, a_t = exp(g_t):
+//     d_t = beta_t (v_t - a_t S_{t-1}^T k_t)
+//     S_t = a_t S_{t-1} + k_t d_t^T,   o_t = scale S_t^T q_t
+// (the state forgets by a, then what it holds for k_t moves towards v_t by
+// beta_t).  By chunks of C = 64 tokens, with c_i = sum of g up to token i of the chunk,
+// D_ij = exp(c_i - c_j) for i >= j and S the state before the chunk:
+//     A  = strict lower part of beta_i D_ij k_i.k_j,   T = (I + A)^{-1}
+//     Y  = V - e^c (K S),   X = beta Y,   V' = T X          (row t of V' is d_t)
+//     P  = scale D_ij q_i.k_j (i >= j),   O = scale e^c (Q S) + P V'
+//     S <- e^{c_last} S + K^T (e^{c_last - c} V')
+// T and P of every chunk are independent of the states and come from
+// delta_prep_kernel; the states are a chain over the chunks (ss2d_delta_chain.cuh).
+//
+// Precision.  The products run on the tensor cores with bfloat16 operands and
+// float32 sums, but nothing is rounded to bfloat16: a float32 operand is the
+// exact sum of three bfloat16 parts (8 bits each), a float16 value of two,
+// and a product of two split operands is the sum of the partial products
+// whose parts' indices add up to less than the number of parts kept (3: what
+// is left out is below 2^-24 of the product, as a float32 rounding is; 2:
+// below 2^-16, used where the result is only rounded to 16 bits).  bfloat16
+// inputs are one part: q.k needs one product and k.S three.  States, sums of
+// g (in double within a chunk: differences of near tokens behind a large
+// sum keep float32 accuracy) and everything elementwise stay float32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ss2d_kernels.cuh"
+
+namespace ss2d {
+
+constexpr int kDeltaC = 64;         // tokens per chunk
+constexpr int kDeltaMaxDK = 128;
+constexpr int kDeltaMaxDV = 256;
+// exp(g) of anything below is 0 in float32; a finite floor keeps sums of g finite (g = -inf forgets all)
+constexpr float kDeltaGFloor = -200.f;
+
+struct DeltaParams {
+    const void *q, *k, *v;         // token rows: HK x DK (q, k), H x DV (v)
+    long long qs, ks, vs;          // values between tokens
+    const float *g, *beta;         // (tokens, H)
+    const int *cu;                 // first token of each sequence (nseq + 1), or null: nseq sequences of L
+    const float *h0;               // (nseq, H, DK, DV) or null
+    float *h_last;                 // (nseq, H, DK, DV) or null
+    void *o;                       // (tokens, H, DV)
+    long long T;                   // tokens
+    int nseq, L, HK, H, DK, DV;
+    int reverse;                   // a sequence is read from its last token to its first
+    float scale;
+    // step: states and the row of the pool that each sequence uses
+    float *pool;
+    const int *slots;
+    long long npool;
+    // scratch of the chunks
+    int NC;                        // chunk slots per sequence (cu null)
+    long long nslots;
+    void *kp, *qp;                 // bf16 parts of k and q per (slot, key head): [NPI][64][DKP]
+    void *Tp, *Pp;                 // bf16 parts of T and P per (slot, head): [parts][64][64]
+    float *vec;                    // per (slot, head): e^c, e^{c_last - c}, beta (64 each)
+    // backward
+    const void *dout;              // gradient of o
+    const float *dh_last;
+    float *dh0;
+    void *dq, *dk, *dv;
+    float *dg, *dbeta;
+    float *Sx, *dSx;               // S before, dS after each chunk: [DV][DKP] per (slot, head)
+    float *Vx, *Yx, *dXx;          // V', Y, dX: [DV][64] per (slot, head)
+    float *klx;                    // e^{c_last - c} V'.(K dS) over 16 columns: [DV / 16][64] per (slot, head)
+};
+
+struct DeltaSeq {
+    long long start;
+    int len;
+};
+// sequence s, held inside the tokens whatever cu says
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaParams &p, int s)
+{
+    if (!p.cu)
+        return {(long long)s * p.L, p.L};
+    long long a = p.cu[s], b = p.cu[s + 1];
+    a = a < 0 ? 0 : (a > p.T ? p.T : a);
+    b = b < a ? a : (b > p.T ? p.T : b);
+    return {a, (int)(b - a)};
+}
+// first chunk slot of a sequence: ceil(len / 64) slots from here never reach
+// the next sequence's, nor floor(T / 64) + nseq
+__device__ __forceinline__ long long delta_slot0(const DeltaParams &p, int s, const DeltaSeq &q)
+{
+    return p.cu ? q.start / kDeltaC + s : (long long)s * p.NC;
+}
+// the (sequence, chunk) of a slot; false: the slot holds none
+__device__ __forceinline__ bool delta_slot(const DeltaParams &p, long long slot, int &s, DeltaSeq &q, int &c)
+{
+    if (!p.cu) {
+        s = (int)(slot / p.NC);
+        c = (int)(slot - (long long)s * p.NC);
+        q = delta_seq(p, s);
+    } else {
+        int lo = 0, hi = p.nseq - 1;   // the last sequence that starts at or before the slot
+        while (lo < hi) {
+            const int m = (lo + hi + 1) >> 1;
+            const DeltaSeq t = delta_seq(p, m);
+            if (delta_slot0(p, m, t) <= slot)
+                lo = m;
+            else
+                hi = m - 1;
+        }
+        s = lo;
+        q = delta_seq(p, s);
+        const long long d = slot - delta_slot0(p, s, q);
+        if (d < 0 || d * kDeltaC >= q.len)
+            return false;
+        c = (int)d;
+    }
+    return (long long)c * kDeltaC < q.len;
+}
+// token that step t of a sequence reads
+__device__ __forceinline__ long long delta_token(const DeltaParams &p, const DeltaSeq &q, int t)
+{
+    return q.start + (p.reverse ? q.len - 1 - t : t);
+}
+
+// ---- bf16 parts ------------------------------------------------------------
+template <typename T>
+struct DeltaParts;   // parts that hold a value of the type exactly
+template <>
+struct DeltaParts<__nv_bfloat16> {
+    static constexpr int n = 1;
+};
+template <>
+struct DeltaParts<__half> {
+    static constexpr int n = 2;
+};
+template <>
+struct DeltaParts<float> {
+    static constexpr int n = 3;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// the first N bf16 parts of (x, y), packed
+template <int N>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&o)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        o[i] = pack_bf16(x, y);
+        if (i + 1 < N) {
+            x -= __uint_as_float(o[i] << 16);
+            y -= __uint_as_float(o[i] & 0xffff0000u);
+        }
+    }
+}
+
+// ---- tensor-core and shared-memory pieces ------------------------------------
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16u : 0u)
+                 : "memory");
+}
+// byte offset of the 16-byte piece `pc` of row `r` in a tile of rows of RB
+// bytes (a multiple of 128): pieces of eight neighbouring rows fall into
+// eight different bank groups, for ldmatrix by rows and by columns
+template <int RB>
+__device__ __forceinline__ uint32_t swz(int r, int pc)
+{
+    return (uint32_t)(r * RB + ((pc ^ (r & 7)) << 4));
+}
+// C fragments of two neighbouring 8-column tiles as the A operand of the 16
+// columns they span, in N parts
+template <int N>
+__device__ __forceinline__ void frag_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&a)[N][4])
+{
+    uint32_t t[N];
+    split2<N>(c0[0], c0[1], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        a[i][0] = t[i];
+    split2<N>(c0[2], c0[3], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        a[i][1] = t[i];
+    split2<N>(c1[0], c1[1], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        a[i][2] = t[i];
+    split2<N>(c1[2], c1[3], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        a[i][3] = t[i];
+}
+
+// ---- token by token ----------------------------------------------------------
+// The recurrence as it stands, for sequences of a few tokens and for one token
+// of many sequences with the states updated in place.  A CTA holds DVT columns
+// of one state in registers, thread (row group rg, four columns): k.S and q.S
+// need one pass over the rows and one sum over the row groups, since
+// o = scale (a q.S + (q.k) d).  Bound by reading and writing the states
+// once: DK * DVT * 8 bytes per CTA, in 16-byte pieces along DV.
+constexpr int kRecurThreads = 256;
+constexpr int kRecurRows = 16;   // rows of the state per thread
+
+template <typename Tin>
+__global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaParams p, int DVT)
+{
+    __shared__ float sk[kDeltaMaxDK], sq[kDeltaMaxDK];
+    __shared__ __align__(16) float red[2][kRecurThreads][4];
+    __shared__ float sqk;
+    const int tid = threadIdx.x;
+    const int nv4 = DVT / 4, RG = kRecurThreads / nv4;
+    const int c4 = tid % nv4, rg = tid / nv4;
+    const int h = blockIdx.y, hk = h / (p.H / p.HK);
+    const int dv0 = blockIdx.x * DVT + c4 * 4;
+    const bool on = rg < RG && dv0 < p.DV;
+    for (long long sn = blockIdx.z; sn < p.nseq; sn += gridDim.z) {
+        const DeltaSeq q = delta_seq(p, (int)sn);
+        long long si = sn;   // state read and written
+        bool live = true;
+        if (p.pool && p.slots) {
+            si = p.slots[sn];
+            live = si >= 0 && si < p.npool;
+            bool dup = false;   // the first sequence of a slot has it
+            for (long long i = tid; i < sn; i += kRecurThreads)
+                dup |= p.slots[i] == (int)si;
+            live = !__syncthreads_or(dup) && live;
+        }
+        const long long srow = (si * p.H + h) * p.DK;
+        float4 S[kRecurRows];
+#pragma unroll
+        for (int i = 0; i < kRecurRows; ++i) {
+            const int r = rg + i * RG;
+            S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *src = p.pool ? p.pool : p.h0;
+            if (on && live && r < p.DK && src)
+                S[i] = *reinterpret_cast<const float4 *>(src + (srow + r) * p.DV + dv0);
+        }
+        for (int t = 0; t < q.len; ++t) {
+            const long long tok = delta_token(p, q, t);
+            __syncthreads();
+            if (tid < 2 * kDeltaMaxDK) {
+                const int i = tid % kDeltaMaxDK;
+                const Tin *src = tid < kDeltaMaxDK ? static_cast<const Tin *>(p.k) + tok * p.ks
+                                                   : static_cast<const Tin *>(p.q) + tok * p.qs;
+                const float v = live && i < p.DK ? to_f32(src[(long long)hk * p.DK + i]) : 0.f;
+                (tid < kDeltaMaxDK ? sk : sq)[i] = v;
+            }
+            __syncthreads();
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll
+            for (int i = 0; i < kRecurRows; ++i) {
+                const int r = rg + i * RG;
+                if (r < p.DK) {
+                    const float kv = sk[r], qv = sq[r];
+                    a.x = fmaf(kv, S[i].x, a.x);
+                    a.y = fmaf(kv, S[i].y, a.y);
+                    a.z = fmaf(kv, S[i].z, a.z);
+                    a.w = fmaf(kv, S[i].w, a.w);
+                    b.x = fmaf(qv, S[i].x, b.x);
+                    b.y = fmaf(qv, S[i].y, b.y);
+                    b.z = fmaf(qv, S[i].z, b.z);
+                    b.w = fmaf(qv, S[i].w, b.w);
+                }
+            }
+            *reinterpret_cast<float4 *>(red[0][tid]) = a;
+            *reinterpret_cast<float4 *>(red[1][tid]) = b;
+            if (tid < 32) {
+                float s = 0.f;
+                for (int i = tid; i < p.DK; i += 32)
+                    s = fmaf(sk[i], sq[i], s);
+                for (int m = 16; m; m >>= 1)
+                    s += __shfl_xor_sync(0xffffffffu, s, m);
+                if (tid == 0)
+                    sqk = s;
+            }
+            __syncthreads();
+            a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < RG; ++i) {
+                const float4 x = *reinterpret_cast<const float4 *>(red[0][i * nv4 + c4]);
+                const float4 y = *reinterpret_cast<const float4 *>(red[1][i * nv4 + c4]);
+                a.x += x.x;
+                a.y += x.y;
+                a.z += x.z;
+                a.w += x.w;
+                b.x += y.x;
+                b.y += y.y;
+                b.z += y.z;
+                b.w += y.w;
+            }
+            if (on && live) {
+                const float gv = p.g[tok * p.H + h], be = p.beta[tok * p.H + h];
+                const float al = expf(gv < kDeltaGFloor ? kDeltaGFloor : gv);
+                const Tin *vr = static_cast<const Tin *>(p.v) + tok * p.vs + (long long)h * p.DV + dv0;
+                float4 d;
+                d.x = be * (to_f32(vr[0]) - al * a.x);
+                d.y = be * (to_f32(vr[1]) - al * a.y);
+                d.z = be * (to_f32(vr[2]) - al * a.z);
+                d.w = be * (to_f32(vr[3]) - al * a.w);
+#pragma unroll
+                for (int i = 0; i < kRecurRows; ++i) {
+                    const int r = rg + i * RG;
+                    if (r < p.DK) {
+                        const float kv = sk[r];
+                        S[i].x = fmaf(kv, d.x, al * S[i].x);
+                        S[i].y = fmaf(kv, d.y, al * S[i].y);
+                        S[i].z = fmaf(kv, d.z, al * S[i].z);
+                        S[i].w = fmaf(kv, d.w, al * S[i].w);
+                    }
+                }
+                if (rg == 0) {
+                    const float w[4] = {p.scale * fmaf(sqk, d.x, al * b.x), p.scale * fmaf(sqk, d.y, al * b.y),
+                                        p.scale * fmaf(sqk, d.z, al * b.z), p.scale * fmaf(sqk, d.w, al * b.w)};
+                    Tin *orow = static_cast<Tin *>(p.o) + (tok * p.H + h) * p.DV + dv0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (std::is_same_v<Tin, float>)
+                            orow[j] = w[j];
+                        else if constexpr (std::is_same_v<Tin, __half>)
+                            orow[j] = __float2half_rn(w[j]);
+                        else
+                            orow[j] = __float2bfloat16_rn(w[j]);
+                    }
+                }
+            } else if (on && rg == 0) {
+                Tin *orow = static_cast<Tin *>(p.o) + (tok * p.H + h) * p.DV + dv0;
+                for (int j = 0; j < 4; ++j)
+                    orow[j] = Tin(0.f);
+            }
+        }
+        float *dst = p.pool ? p.pool : p.h_last;
+        if (on && live && dst) {
+#pragma unroll
+            for (int i = 0; i < kRecurRows; ++i) {
+                const int r = rg + i * RG;
+                if (r < p.DK)
+                    *reinterpret_cast<float4 *>(dst + (srow + r) * p.DV + dv0) = S[i];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- chunk preparation ---------------------------------------------------------
+// Per (slot, key head): the bf16 parts of K and Q (scratch copies unless the
+// inputs are bf16 already), K K^T and Q K^T on the tensor cores, and for each
+// value head of the group T and P in bf16 parts and the chunk's e^c,
+// e^{c_last - c}, beta.  Steps past the sequence's end have k = q = 0, g = 0,
+// beta = 0: they leave the state as it is.
+//
+// 4 warps, warp w the chunk's rows 16 w .. 16 w + 15.  T = (I + A)^{-1} by
+// forward substitution in float32, thread j its column j with the column in
+// registers; A's rows are broadcast reads.
+constexpr int kPrepThreads = 128;
+
+template <int DKP, int NPI>
+__host__ __device__ constexpr int delta_prep_smem()
+{
+    return 2 * NPI * kDeltaC * DKP * 2 > kDeltaC * 64 * 4 ? 2 * NPI * kDeltaC * DKP * 2 : kDeltaC * 64 * 4;
+}
+
+// NPI x 64 x DKP bf16 parts of the token rows of q or k into a swizzled tile
+template <typename Tin, int DKP, int NPI>
+__device__ __forceinline__ void delta_stage_parts(const DeltaParams &p, const void *base, long long ts, int hk,
+                                                  const DeltaSeq &q, int t0, unsigned char *tile, int nthreads)
+{
+    constexpr int RB = DKP * 2, PPR = DKP / 8;
+    const Tin *src = static_cast<const Tin *>(base) + (long long)hk * p.DK;
+    for (int i = threadIdx.x; i < kDeltaC * PPR; i += nthreads) {
+        const int r = i / PPR, pc = i % PPR;
+        const bool in = t0 + r < q.len && pc * 8 < p.DK;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = 0.f;
+        if (in) {
+            const Tin *row = src + delta_token(p, q, t0 + r) * ts + pc * 8;
+            if constexpr (sizeof(Tin) == 2) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(row);
+                if constexpr (NPI == 1) {
+                    *reinterpret_cast<uint4 *>(tile + swz<RB>(r, pc)) = u;
+                    continue;
+                }
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[2 * j] = half_bits_to_f32<Tin>(w[j] & 0xffffu);
+                    v[2 * j + 1] = half_bits_to_f32<Tin>(w[j] >> 16);
+                }
+            } else {
+                const float4 f0 = *reinterpret_cast<const float4 *>(row);
+                const float4 f1 = *reinterpret_cast<const float4 *>(row + 4);
+                v[0] = f0.x;
+                v[1] = f0.y;
+                v[2] = f0.z;
+                v[3] = f0.w;
+                v[4] = f1.x;
+                v[5] = f1.y;
+                v[6] = f1.z;
+                v[7] = f1.w;
+            }
+        }
+        uint32_t w[4][NPI];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            split2<NPI>(v[2 * j], v[2 * j + 1], w[j]);
+#pragma unroll
+        for (int n = 0; n < NPI; ++n)
+            *reinterpret_cast<uint4 *>(tile + n * kDeltaC * RB + swz<RB>(r, pc)) =
+                make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+    }
+}
+
+// acc (16 rows x 8 NT columns of a warp) += rows r0.. of tile A times rows n0.. of tile B, transposed: sums over DKP
+template <int DKP, int NPI, int NT>
+__device__ __forceinline__ void delta_rows_product(uint32_t A, uint32_t B, int r0, int n0, float (&acc)[NT][4])
+{
+    constexpr int RB = DKP * 2, PB = kDeltaC * RB;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int ks = 0; ks < DKP / 16; ++ks) {
+        uint32_t a[NPI][4];
+#pragma unroll
+        for (int n = 0; n < NPI; ++n)
+            ldsm4(A + n * PB + swz<RB>(r0 + (lane & 15), ks * 2 + (lane >> 4)), a[n]);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt += 2) {
+#pragma unroll
+            for (int m = 0; m < NPI; ++m) {
+                uint32_t b[4];
+                ldsm4(B + m * PB + swz<RB>(n0 + nt * 8 + (lane & 7) + (lane >> 4) * 8, ks * 2 + (lane >> 3 & 1)), b);
+#pragma unroll
+                for (int n = 0; n < NPI && n + m < NPI; ++n) {
+                    mma16816(acc[nt], a[n], b[0], b[1]);
+                    mma16816(acc[nt + 1], a[n], b[2], b[3]);
+                }
+            }
+        }
+    }
+}
+
+// c (as a float and what it lacks) and beta of one head's chunk, by one warp: lane l holds tokens 2l, 2l + 1
+__device__ __forceinline__ void delta_decays(const DeltaParams &p, const DeltaSeq &q, int t0, int h, float *ch,
+                                             float *cl, float *be)
+{
+    const int lane = threadIdx.x & 31;
+    double v[2];
+    float b[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int t = t0 + 2 * lane + j;
+        float gv = 0.f;
+        b[j] = 0.f;
+        if (t < q.len) {
+            const long long i = delta_token(p, q, t) * p.H + h;
+            gv = p.g[i];
+            gv = gv < kDeltaGFloor ? kDeltaGFloor : gv;   // a NaN stays one
+            b[j] = p.beta[i];
+        }
+        v[j] = (double)gv;
+    }
+    double s = v[0] + v[1];
+    for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o)
+            s += u;
+    }
+    const double c1 = s, c0 = s - v[1];
+    ch[2 * lane] = (float)c0;
+    cl[2 * lane] = (float)(c0 - (double)(float)c0);
+    ch[2 * lane + 1] = (float)c1;
+    cl[2 * lane + 1] = (float)(c1 - (double)(float)c1);
+    be[2 * lane] = b[0];
+    be[2 * lane + 1] = b[1];
+}
+
+// NPT parts of T, NPP of P are written
+template <typename Tin, int DKP, int NPT, int NPP>
+__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaParams p)
+{
+    constexpr int NPI = DeltaParts<Tin>::n, RB = DKP * 2, PB = kDeltaC * RB;
+    extern __shared__ __align__(128) unsigned char dsm[];
+    __shared__ float ch[kDeltaC], cl[kDeltaC], be[kDeltaC];
+    int s, c;
+    DeltaSeq q;
+    if (!delta_slot(p, blockIdx.x, s, q, c))
+        return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = blockIdx.y, G = p.H / p.HK, t0 = c * kDeltaC;
+    unsigned char *kt = dsm, *qt = dsm + NPI * PB;
+    delta_stage_parts<Tin, DKP, NPI>(p, p.k, p.ks, hk, q, t0, kt, kPrepThreads);
+    delta_stage_parts<Tin, DKP, NPI>(p, p.q, p.qs, hk, q, t0, qt, kPrepThreads);
+    __syncthreads();
+    if (NPI > 1) {   // scratch copies, rows in order (not swizzled)
+        const long long base = ((long long)blockIdx.x * p.HK + hk) * NPI * PB;
+        for (int i = tid; i < NPI * kDeltaC * (DKP / 8); i += kPrepThreads) {
+            const int r = i / (DKP / 8), pc = i % (DKP / 8);   // r counts the parts' rows
+            const uint32_t so = (uint32_t)(r / kDeltaC) * PB + swz<RB>(r % kDeltaC, pc);
+            *reinterpret_cast<uint4 *>(static_cast<char *>(p.kp) + base + (long long)i * 16) =
+                *reinterpret_cast<const uint4 *>(kt + so);
+            *reinterpret_cast<uint4 *>(static_cast<char *>(p.qp) + base + (long long)i * 16) =
+                *reinterpret_cast<const uint4 *>(qt + so);
+        }
+    }
+    float kk[8][4], qk[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            kk[n][j] = qk[n][j] = 0.f;
+    delta_rows_product<DKP, NPI, 8>(smem_addr(kt), smem_addr(kt), warp * 16, 0, kk);
+    delta_rows_product<DKP, NPI, 8>(smem_addr(qt), smem_addr(kt), warp * 16, 0, qk);
+    float *As = reinterpret_cast<float *>(dsm);   // [64][64], over the tiles
+    const int r0 = warp * 16 + (lane >> 2);
+    for (int hi = 0; hi < G; ++hi) {
+        const int h = hk * G + hi;
+        const long long sh = (long long)blockIdx.x * p.H + h;
+        __syncthreads();   // the tiles (or the last head's A) are read
+        if (warp == 0)
+            delta_decays(p, q, t0, h, ch, cl, be);
+        __syncthreads();
+        if (tid < kDeltaC) {
+            float *vec = p.vec + sh * 3 * kDeltaC;
+            vec[tid] = expf(ch[tid] + cl[tid]);
+            vec[kDeltaC + tid] = expf((ch[kDeltaC - 1] - ch[tid]) + (cl[kDeltaC - 1] - cl[tid]));
+            vec[2 * kDeltaC + tid] = be[tid];
+        }
+        uint32_t *P = static_cast<uint32_t *>(p.Pp) + sh * NPP * (kDeltaC * kDeltaC / 2);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int j0 = n * 8 + (lane & 3) * 2;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = r0 + hf * 8;
+                float pv[2], av[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = j0 + e;
+                    const float D = j <= i ? expf((ch[i] - ch[j]) + (cl[i] - cl[j])) : 0.f;
+                    pv[e] = j <= i ? p.scale * D * qk[n][hf * 2 + e] : 0.f;
+                    av[e] = j < i ? be[i] * D * kk[n][hf * 2 + e] : 0.f;
+                }
+                *reinterpret_cast<float2 *>(As + i * kDeltaC + j0) = make_float2(av[0], av[1]);
+                // blocks above the diagonal 16 x 16 blocks are never read
+                if (n / 2 <= warp) {
+                    uint32_t w[NPP];
+                    split2<NPP>(pv[0], pv[1], w);
+#pragma unroll
+                    for (int m = 0; m < NPP; ++m)
+                        P[m * (kDeltaC * kDeltaC / 2) + (i * kDeltaC + j0) / 2] = w[m];
+                }
+            }
+        }
+        __syncthreads();
+        if (tid < kDeltaC) {
+            // column j = tid of T: T_ij = delta_ij - sum_{m < i} A_im T_mj; a warp's columns start at row 32 * warp
+            __nv_bfloat16 *Tg = static_cast<__nv_bfloat16 *>(p.Tp) + sh * NPT * (kDeltaC * kDeltaC) + tid;
+            float col[kDeltaC];
+#pragma unroll
+            for (int i = 0; i < kDeltaC; ++i) {
+                float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+                if (i >= 32 || warp == 0) {
+#pragma unroll
+                    for (int m = 0; m < i; m += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(As + i * kDeltaC + m);
+                        a0 = fmaf(w.x, col[m], a0);
+                        if (m + 1 < i)
+                            a1 = fmaf(w.y, col[m + 1], a1);
+                        if (m + 2 < i)
+                            a2 = fmaf(w.z, col[m + 2], a2);
+                        if (m + 3 < i)
+                            a3 = fmaf(w.w, col[m + 3], a3);
+                    }
+                }
+                const float v = (i == tid ? 1.f : 0.f) - ((a0 + a1) + (a2 + a3));
+                col[i] = i < tid ? 0.f : v;
+                float x = col[i];
+                if (tid / 16 <= i / 16) {
+#pragma unroll
+                    for (int m = 0; m < NPT; ++m) {
+                        const __nv_bfloat16 b = __float2bfloat16_rn(x);
+                        Tg[m * (kDeltaC * kDeltaC) + i * kDeltaC] = b;
+                        x -= __bfloat162float(b);
+                    }
+                }
+            }
+        }
+    }
+}
+
+}  // namespace ss2d

@@ -1,0 +1,9 @@
+// ss2d_delta_f16.cu -- the gated delta rule's kernels for __half inputs.
+#include "ss2d_delta_launch.cuh"
+
+namespace ss2d {
+cudaError_t launch_delta_f16(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st)
+{
+    return launch_delta<__half>(p, pl, what, st);
+}
+}  // namespace ss2d

@@ -1,0 +1,24 @@
+// ss2d_delta_launch.h -- internal interface between the gated delta rule's C
+// ABI (ss2d_delta.cu) and its kernels, one translation unit per input type.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "ss2d_delta.cuh"
+
+namespace ss2d {
+
+// Layout of a chunked call's scratch, per chunk slot and head.
+struct DeltaPlan {
+    int dkp;       // DK padded to 64 or 128
+    int npi;       // bf16 parts of an input value
+    int np, npp;   // parts of T, of P
+};
+
+cudaError_t launch_delta_bf16(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st);
+cudaError_t launch_delta_f16(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st);
+cudaError_t launch_delta_f32(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st);
+// what: the recurrent kernel, the chunked forward, the backward
+enum { kDeltaRecur = 0, kDeltaFwd = 1, kDeltaBwd = 2 };
+
+}  // namespace ss2d

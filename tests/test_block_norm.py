@@ -290,14 +290,15 @@ def test_slices_of_a_projection(off):
     one = binding.block_norm_fwd(x, z=z, post="rms", w_post=w)[0]
     two = binding.block_norm_fwd(x.contiguous(), z=z.contiguous(), post="rms", w_post=w)[0]
     three = binding.block_norm_fwd(x.contiguous(), z=z, post="rms", w_post=w)[0]
-    # the vector and the single-value kernels add a row's squares in another order
-    bound = 2 ** -8 * two.float().abs() + 1e-6
-    assert torch.all((one.float() - two.float()).abs() <= bound) and torch.equal(one, three)
+    # the vector and the single-value kernels add a row's squares in another order; both then round to bfloat16, half
+    # a step (up to 2^-8 of the value) each
+    far = (one.float() - two.float()).abs() - 2 ** -7 * two.float().abs() - 1e-6
+    assert float(far.max()) <= 0 and torch.equal(one, three)
     g1 = binding.block_norm_bwd(x, two, z=z, post="rms", w_post=w, residual=False)
     g2 = binding.block_norm_bwd(x.contiguous(), two, z=z.contiguous(), post="rms", w_post=w, residual=False)
     for n in ("dx", "dz", "dw_post"):
         a, b = g1[n].float(), g2[n].float()
-        assert torch.all((a - b).abs() <= 2 ** -8 * b.abs() + 1e-4 * b.abs().max()), n
+        assert float(((a - b).abs() - 2 ** -7 * b.abs() - 1e-4 * b.abs().max()).max()) <= 0, n
     with pytest.raises(ValueError, match="packed rows"):
         binding.block_norm_fwd(wide[:, ::2][:, :D])
 
