@@ -233,6 +233,90 @@ __device__ __forceinline__ void frag_a(const float (&c0)[4], const float (&c1)[4
         a[i][3] = t[i];
 }
 
+// c0, c1 (16 x 8 each) += A parts (NA) times B parts (NB), the products whose
+// part indices add up to less than KEEP.  The tensor cores' sums truncate
+// (each accumulation loses up to 2^-23 of the sum, always downwards), so
+// three-part products are summed from zero, smallest parts first, and added to
+// the result by a rounding float32 addition: measured on the float32 backward
+// (32 x 64 heads, 1500 tokens) the gradients are 2.8e-7 off instead of 3.8e-6.  The
+// additions issue in the tensor pipe's shadow.
+template <int NA, int NB, int KEEP>
+__device__ __forceinline__ void mma_parts(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
+                                          const uint32_t (&b)[NB][4])
+{
+    if constexpr (KEEP == 3) {
+        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int sum = KEEP - 1; sum >= 0; --sum)
+#pragma unroll
+            for (int m = 0; m < NB; ++m)
+                if (sum - m >= 0 && sum - m < NA) {
+                    mma16816(d0, a[sum - m], b[m][0], b[m][1]);
+                    mma16816(d1, a[sum - m], b[m][2], b[m][3]);
+                }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c0[j] += d0[j];
+            c1[j] += d1[j];
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < NB; ++m)
+#pragma unroll
+            for (int n = 0; n < NA; ++n)
+                if (n + m < KEEP) {
+                    mma16816(c0, a[n], b[m][0], b[m][1]);
+                    mma16816(c1, a[n], b[m][2], b[m][3]);
+                }
+    }
+}
+
+// B from rows of a [n][k] tile: B element (k, n) is row n, column k
+template <int RB, int NA, int NB, int KEEP>
+__device__ __forceinline__ void mma_rows(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], uint32_t tile,
+                                         int part, int row, int piece)
+{
+    constexpr int NL = NB < KEEP ? NB : KEEP;
+    const int lane = threadIdx.x & 31;
+    uint32_t b[NL][4];
+#pragma unroll
+    for (int m = 0; m < NL; ++m)
+        ldsm4(tile + m * part + swz<RB>(row + (lane & 7) + (lane >> 4) * 8, piece + (lane >> 3 & 1)), b[m]);
+    mma_parts<NA, NL, KEEP>(c0, c1, a, b);
+}
+// B from a [k][n] tile: rows k, columns n
+template <int RB, int NA, int NB, int KEEP>
+__device__ __forceinline__ void mma_cols(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], uint32_t tile,
+                                         int part, int row, int piece)
+{
+    constexpr int NL = NB < KEEP ? NB : KEEP;
+    const int lane = threadIdx.x & 31;
+    uint32_t b[NL][4];
+#pragma unroll
+    for (int m = 0; m < NL; ++m)
+        ldsm4t(tile + m * part + swz<RB>(row + (lane & 15), piece + (lane >> 4)), b[m]);
+    mma_parts<NA, NL, KEEP>(c0, c1, a, b);
+}
+
+// A fragment (rows m0.., columns k0..) of a tile stored [k][m] in rows of 128 bytes
+template <int N>
+__device__ __forceinline__ void frag_t(uint32_t tile, int part, int k0, int m0, uint32_t (&a)[N][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        ldsm4t(tile + n * part + swz<128>(k0 + (lane & 7) + (lane >> 4) * 8, m0 / 8 + (lane >> 3 & 1)), a[n]);
+}
+// the same of a tile stored [m][k]
+template <int N>
+__device__ __forceinline__ void frag_n(uint32_t tile, int part, int m0, int k0, uint32_t (&a)[N][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        ldsm4(tile + n * part + swz<128>(m0 + (lane & 15), k0 / 8 + (lane >> 4)), a[n]);
+}
+
 // ---- token by token ----------------------------------------------------------
 // The recurrence as it stands, for sequences of a few tokens and for one token
 // of many sequences with the states updated in place.  A CTA holds DVT columns
@@ -389,16 +473,26 @@ __global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaP
 // e^{c_last - c}, beta.  Steps past the sequence's end have k = q = 0, g = 0,
 // beta = 0: they leave the state as it is.
 //
-// 4 warps, warp w the chunk's rows 16 w .. 16 w + 15.  T = (I + A)^{-1} by
-// forward substitution in float32, thread j its column j with the column in
-// registers; A's rows are broadcast reads.
+// 4 warps, warp w the chunk's rows 16 w .. 16 w + 15 of the products.  T = (I + A)^{-1}
+// in 16 x 16 blocks: warp w inverts block (w, w) by forward substitution in
+// float32 (lane j its column j), then has the blocks below it,
+//     T_iw = -T_ii sum_{w <= m < i} A_im T_mw,   i = w + 1 .. 3,
+// as tensor-core products of bf16 parts, transposed like the chain's, so that
+// each result is the next product's A operand.  (One thread per column of the
+// whole 64 x 64 substitution, the first form, waited on 64 dependent rows: 363 us
+// for 6144 chunks of 64 x 64 heads.)  T and P leave through shared memory in
+// 16-byte pieces, the blocks above the diagonal not at all.
 constexpr int kPrepThreads = 128;
 
-template <int DKP, int NPI>
-__host__ __device__ constexpr int delta_prep_smem()
-{
-    return 2 * NPI * kDeltaC * DKP * 2 > kDeltaC * 64 * 4 ? 2 * NPI * kDeltaC * DKP * 2 : kDeltaC * 64 * 4;
-}
+template <int DKP, int NPI, int NPT, int NPP>
+struct PrepLayout {
+    static constexpr int PB = kDeltaC * 128;                   // one part of A, T or P
+    static constexpr int oX = NPT * PB;                        // P, then T; A before it
+    static constexpr int oD = oX + (NPT > NPP ? NPT : NPP) * PB;
+    static constexpr int head = oD + 4 * 16 * 20 * 4;          // diagonal blocks of A, rows of 20 floats
+    static constexpr int tiles = 2 * NPI * kDeltaC * DKP * 2;  // K and Q, read before the heads
+    static constexpr int bytes = tiles > head ? tiles : head;
+};
 
 // NPI x 64 x DKP bf16 parts of the token rows of q or k into a swizzled tile
 template <typename Tin, int DKP, int NPI>
@@ -466,16 +560,12 @@ __device__ __forceinline__ void delta_rows_product(uint32_t A, uint32_t B, int r
             ldsm4(A + n * PB + swz<RB>(r0 + (lane & 15), ks * 2 + (lane >> 4)), a[n]);
 #pragma unroll
         for (int nt = 0; nt < NT; nt += 2) {
+            uint32_t b[NPI][4];
 #pragma unroll
-            for (int m = 0; m < NPI; ++m) {
-                uint32_t b[4];
-                ldsm4(B + m * PB + swz<RB>(n0 + nt * 8 + (lane & 7) + (lane >> 4) * 8, ks * 2 + (lane >> 3 & 1)), b);
-#pragma unroll
-                for (int n = 0; n < NPI && n + m < NPI; ++n) {
-                    mma16816(acc[nt], a[n], b[0], b[1]);
-                    mma16816(acc[nt + 1], a[n], b[2], b[3]);
-                }
-            }
+            for (int m = 0; m < NPI; ++m)
+                ldsm4(B + m * PB + swz<RB>(n0 + nt * 8 + (lane & 7) + (lane >> 4) * 8, ks * 2 + (lane >> 3 & 1)),
+                      b[m]);
+            mma_parts<NPI, NPI, 3>(acc[nt], acc[nt + 1], a, b);
         }
     }
 }
@@ -517,8 +607,9 @@ __device__ __forceinline__ void delta_decays(const DeltaParams &p, const DeltaSe
 
 // NPT parts of T, NPP of P are written
 template <typename Tin, int DKP, int NPT, int NPP>
-__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const DeltaParams p)
 {
+    using Lay = PrepLayout<DKP, DeltaParts<Tin>::n, NPT, NPP>;
     constexpr int NPI = DeltaParts<Tin>::n, RB = DKP * 2, PB = kDeltaC * RB;
     extern __shared__ __align__(128) unsigned char dsm[];
     __shared__ float ch[kDeltaC], cl[kDeltaC], be[kDeltaC];
@@ -551,12 +642,22 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaPar
             kk[n][j] = qk[n][j] = 0.f;
     delta_rows_product<DKP, NPI, 8>(smem_addr(kt), smem_addr(kt), warp * 16, 0, kk);
     delta_rows_product<DKP, NPI, 8>(smem_addr(qt), smem_addr(kt), warp * 16, 0, qk);
-    float *As = reinterpret_cast<float *>(dsm);   // [64][64], over the tiles
+    const uint32_t sA = smem_addr(dsm), sX = sA + Lay::oX;
+    float *dg = reinterpret_cast<float *>(dsm + Lay::oD);   // [4][16][20]
     const int r0 = warp * 16 + (lane >> 2);
+    // the lower blocks of N parts from shared memory to a head's part of scratch
+    auto leave = [&](void *dst, int N) {
+        for (int i = tid; i < N * kDeltaC * 8; i += kPrepThreads) {
+            const int r = i >> 3, pc = i & 7, row = r % kDeltaC;   // r counts the parts' rows
+            if (pc / 2 <= row / 16)
+                *reinterpret_cast<uint4 *>(static_cast<char *>(dst) + i * 16) =
+                    *reinterpret_cast<const uint4 *>(dsm + Lay::oX + r / kDeltaC * Lay::PB + swz<128>(row, pc));
+        }
+    };
     for (int hi = 0; hi < G; ++hi) {
         const int h = hk * G + hi;
         const long long sh = (long long)blockIdx.x * p.H + h;
-        __syncthreads();   // the tiles (or the last head's A) are read
+        __syncthreads();   // the tiles (or the last head's T) are read
         if (warp == 0)
             delta_decays(p, q, t0, h, ch, cl, be);
         __syncthreads();
@@ -566,9 +667,10 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaPar
             vec[kDeltaC + tid] = expf((ch[kDeltaC - 1] - ch[tid]) + (cl[kDeltaC - 1] - cl[tid]));
             vec[2 * kDeltaC + tid] = be[tid];
         }
-        uint32_t *P = static_cast<uint32_t *>(p.Pp) + sh * NPP * (kDeltaC * kDeltaC / 2);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
+            if (n / 2 > warp)
+                continue;   // above the diagonal blocks
             const int j0 = n * 8 + (lane & 3) * 2;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -581,51 +683,85 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaPar
                     pv[e] = j <= i ? p.scale * D * qk[n][hf * 2 + e] : 0.f;
                     av[e] = j < i ? be[i] * D * kk[n][hf * 2 + e] : 0.f;
                 }
-                *reinterpret_cast<float2 *>(As + i * kDeltaC + j0) = make_float2(av[0], av[1]);
-                // blocks above the diagonal 16 x 16 blocks are never read
-                if (n / 2 <= warp) {
-                    uint32_t w[NPP];
-                    split2<NPP>(pv[0], pv[1], w);
+                const uint32_t o = swz<128>(i, n) + (lane & 3) * 4;
+                uint32_t w[NPP], u[NPT];
+                split2<NPP>(pv[0], pv[1], w);
 #pragma unroll
-                    for (int m = 0; m < NPP; ++m)
-                        P[m * (kDeltaC * kDeltaC / 2) + (i * kDeltaC + j0) / 2] = w[m];
+                for (int m = 0; m < NPP; ++m)
+                    *reinterpret_cast<uint32_t *>(dsm + Lay::oX + m * Lay::PB + o) = w[m];
+                if (n / 2 < warp) {
+                    split2<NPT>(av[0], av[1], u);
+#pragma unroll
+                    for (int m = 0; m < NPT; ++m)
+                        *reinterpret_cast<uint32_t *>(dsm + m * Lay::PB + o) = u[m];
+                } else {
+                    *reinterpret_cast<float2 *>(dg + (i * 20 + (j0 & 15))) = make_float2(av[0], av[1]);
                 }
             }
         }
         __syncthreads();
-        if (tid < kDeltaC) {
-            // column j = tid of T: T_ij = delta_ij - sum_{m < i} A_im T_mj; a warp's columns start at row 32 * warp
-            __nv_bfloat16 *Tg = static_cast<__nv_bfloat16 *>(p.Tp) + sh * NPT * (kDeltaC * kDeltaC) + tid;
-            float col[kDeltaC];
+        leave(static_cast<char *>(p.Pp) + sh * NPP * Lay::PB, NPP);
+        // column j = lane of the diagonal block's inverse
+        float col[16];
+        if (lane < 16) {
+            const float *a = dg + warp * 16 * 20;
 #pragma unroll
-            for (int i = 0; i < kDeltaC; ++i) {
-                float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-                if (i >= 32 || warp == 0) {
+            for (int i = 0; i < 16; ++i) {
+                float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-                    for (int m = 0; m < i; m += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(As + i * kDeltaC + m);
-                        a0 = fmaf(w.x, col[m], a0);
-                        if (m + 1 < i)
-                            a1 = fmaf(w.y, col[m + 1], a1);
-                        if (m + 2 < i)
-                            a2 = fmaf(w.z, col[m + 2], a2);
-                        if (m + 3 < i)
-                            a3 = fmaf(w.w, col[m + 3], a3);
-                    }
+                for (int m = 0; m < i; m += 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(a + i * 20 + m);
+                    a0 = fmaf(w.x, col[m], a0);
+                    if (m + 1 < i)
+                        a1 = fmaf(w.y, col[m + 1], a1);
+                    if (m + 2 < i)
+                        a0 = fmaf(w.z, col[m + 2], a0);
+                    if (m + 3 < i)
+                        a1 = fmaf(w.w, col[m + 3], a1);
                 }
-                const float v = (i == tid ? 1.f : 0.f) - ((a0 + a1) + (a2 + a3));
-                col[i] = i < tid ? 0.f : v;
-                float x = col[i];
-                if (tid / 16 <= i / 16) {
+                col[i] = (i == lane ? 1.f : 0.f) - (a0 + a1);   // zero above the diagonal by itself
+            }
+        }
+        __syncthreads();   // P has left
+        if (lane < 16) {
 #pragma unroll
-                    for (int m = 0; m < NPT; ++m) {
-                        const __nv_bfloat16 b = __float2bfloat16_rn(x);
-                        Tg[m * (kDeltaC * kDeltaC) + i * kDeltaC] = b;
-                        x -= __bfloat162float(b);
-                    }
+            for (int i = 0; i < 16; ++i) {
+                float x = col[i];
+                unsigned char *o = dsm + Lay::oX + swz<128>(warp * 16 + i, warp * 2 + (lane >> 3)) + (lane & 7) * 2;
+#pragma unroll
+                for (int m = 0; m < NPT; ++m) {
+                    const __nv_bfloat16 b = __float2bfloat16_rn(x);
+                    *reinterpret_cast<__nv_bfloat16 *>(o + m * Lay::PB) = b;
+                    x -= __bfloat162float(b);
                 }
             }
         }
+        __syncthreads();
+        for (int i = warp + 1; i < 4; ++i) {
+            float w0[4] = {0.f, 0.f, 0.f, 0.f}, w1[4] = {0.f, 0.f, 0.f, 0.f}, u0[4] = {0.f, 0.f, 0.f, 0.f},
+                  u1[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t a[NPT][4];
+            for (int m = warp; m < i; ++m) {
+                frag_t<NPT>(sX, Lay::PB, m * 16, warp * 16, a);
+                mma_rows<128, NPT, NPT, NPT>(w0, w1, a, sA, Lay::PB, i * 16, m * 2);
+            }
+            frag_a<NPT>(w0, w1, a);
+            mma_rows<128, NPT, NPT, NPT>(u0, u1, a, sX, Lay::PB, i * 16, i * 2);
+            uint32_t o[4][NPT];
+            split2<NPT>(-u0[0], -u0[1], o[0]);
+            split2<NPT>(-u0[2], -u0[3], o[1]);
+            split2<NPT>(-u1[0], -u1[1], o[2]);
+            split2<NPT>(-u1[2], -u1[3], o[3]);
+#pragma unroll
+            for (int m = 0; m < NPT; ++m) {
+                const uint32_t r[4] = {o[0][m], o[1][m], o[2][m], o[3][m]};
+                stsm4t(sX + m * Lay::PB + swz<128>(i * 16 + (lane & 7) + (lane >> 4) * 8, warp * 2 + (lane >> 3 & 1)),
+                       r);
+            }
+            __syncwarp();
+        }
+        __syncthreads();
+        leave(static_cast<char *>(p.Tp) + sh * NPT * Lay::PB, NPT);
     }
 }
 

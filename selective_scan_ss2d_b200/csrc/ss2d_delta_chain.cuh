@@ -43,49 +43,6 @@ struct ChainLayout {
     static constexpr int bytes = stages * stage + out;
 };
 
-// acc (16 x 8 NT) += A parts times rows of a [n][k] tile: B element (k, n) is row n, columns k
-template <int RB, int NA, int NB, int KEEP>
-__device__ __forceinline__ void mma_rows(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], uint32_t tile,
-                                         int part, int row, int piece)
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int m = 0; m < NB; ++m) {
-        if (m >= KEEP)
-            continue;
-        uint32_t b[4];
-        ldsm4(tile + m * part + swz<RB>(row + (lane & 7) + (lane >> 4) * 8, piece + (lane >> 3 & 1)), b);
-#pragma unroll
-        for (int n = 0; n < NA; ++n) {
-            if (n + m < KEEP) {
-                mma16816(c0, a[n], b[0], b[1]);
-                mma16816(c1, a[n], b[2], b[3]);
-            }
-        }
-    }
-}
-// the same for a [k][n] tile: rows k, columns n
-template <int RB, int NA, int NB, int KEEP>
-__device__ __forceinline__ void mma_cols(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], uint32_t tile,
-                                         int part, int row, int piece)
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int m = 0; m < NB; ++m) {
-        if (m >= KEEP)
-            continue;
-        uint32_t b[4];
-        ldsm4t(tile + m * part + swz<RB>(row + (lane & 15), piece + (lane >> 4)), b);
-#pragma unroll
-        for (int n = 0; n < NA; ++n) {
-            if (n + m < KEEP) {
-                mma16816(c0, a[n], b[0], b[1]);
-                mma16816(c1, a[n], b[2], b[3]);
-            }
-        }
-    }
-}
-
 // NP parts of intermediate values (states, X, V'), NPP of P and of what only the output is made of
 template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP>
 __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaParams p)

@@ -70,25 +70,6 @@ __device__ __forceinline__ void load8(const float *src, float (&v)[8])
     v[6] = b.z;
     v[7] = b.w;
 }
-// A fragment (rows m0.., columns k0..) of a tile stored [k][m] in rows of 128 bytes
-template <int N>
-__device__ __forceinline__ void frag_t(uint32_t tile, int part, int k0, int m0, uint32_t (&a)[N][4])
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        ldsm4t(tile + n * part + swz<128>(k0 + (lane & 7) + (lane >> 4) * 8, m0 / 8 + (lane >> 3 & 1)), a[n]);
-}
-// the same of a tile stored [m][k]
-template <int N>
-__device__ __forceinline__ void frag_n(uint32_t tile, int part, int m0, int k0, uint32_t (&a)[N][4])
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        ldsm4(tile + n * part + swz<128>(m0 + (lane & 15), k0 / 8 + (lane >> 4)), a[n]);
-}
-
 template <typename Tin, int DKP>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const DeltaParams p)
 {

@@ -18,7 +18,7 @@ cudaError_t delta_smem(void (*kern)(A...), int bytes)
 template <typename Tin, int DKP, int NPT, int NPP>
 cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
 {
-    constexpr int smem = delta_prep_smem<DKP, DeltaParts<Tin>::n>();
+    constexpr int smem = PrepLayout<DKP, DeltaParts<Tin>::n, NPT, NPP>::bytes;
     auto kern = delta_prep_kernel<Tin, DKP, NPT, NPP>;
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
