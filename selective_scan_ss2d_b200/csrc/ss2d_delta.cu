@@ -109,13 +109,12 @@ int run_chunked(Call &c, bool bwd)
     p.nslots = p.cu ? p.T / kDeltaC + p.nseq : (long long)p.nseq * p.NC;
     if (p.nslots > INT_MAX || p.HK > 65535)
         return SS2D_ERR_SHAPE;
-    const size_t n = (size_t)p.nslots, nh = n * p.H, part = (size_t)kDeltaC * kDeltaC * 2;
+    const size_t n = (size_t)p.nslots, nh = n * p.H, part = ss2d::kTriBytes;
     const size_t kp = pl.npi > 1 ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
     const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
-    const size_t kl = bwd ? nh * (p.DV / 16) * kDeltaC * 4 : 0;
-    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx, vx, kl};
-    size_t off[11], total = 0;
-    for (int i = 0; i < 11; ++i) {
+    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx, vx};
+    size_t off[10], total = 0;
+    for (int i = 0; i < 10; ++i) {
         off[i] = total;
         total += up256(size[i]);
     }
@@ -135,7 +134,6 @@ int run_chunked(Call &c, bool bwd)
     p.Vx = f(7);
     p.Yx = f(8);
     p.dXx = f(9);
-    p.klx = f(10);
     rc = run(c, pl, bwd ? ss2d::kDeltaBwd : ss2d::kDeltaFwd);
     const cudaError_t e = cudaFreeAsync(scratch, c.st);
     if (rc == SS2D_OK && e != cudaSuccess) {

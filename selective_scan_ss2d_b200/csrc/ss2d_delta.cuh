@@ -63,7 +63,7 @@ struct DeltaParams {
     int NC;                        // chunk slots per sequence (cu null)
     long long nslots;
     void *kp, *qp;                 // bf16 parts of k and q per (slot, key head): [NPI][64][DKP]
-    void *Tp, *Pp;                 // bf16 parts of T and P per (slot, head): [parts][64][64]
+    void *Tp, *Pp;                 // bf16 parts of T and P per (slot, head), packed blocks
     float *vec;                    // per (slot, head): e^c, e^{c_last - c}, beta (64 each)
     // backward
     const void *dout;              // gradient of o
@@ -73,7 +73,6 @@ struct DeltaParams {
     float *dg, *dbeta;
     float *Sx, *dSx;               // S before, dS after each chunk: [DV][DKP] per (slot, head)
     float *Vx, *Yx, *dXx;          // V', Y, dX: [DV][64] per (slot, head)
-    float *klx;                    // e^{c_last - c} V'.(K dS) over 16 columns: [DV / 16][64] per (slot, head)
 };
 
 struct DeltaSeq {
@@ -209,6 +208,12 @@ __device__ __forceinline__ uint32_t swz(int r, int pc)
 {
     return (uint32_t)(r * RB + ((pc ^ (r & 7)) << 4));
 }
+// A lower triangular 64 x 64 bf16 part as its ten 16 x 16 blocks (bi >= bj), 512
+// bytes each, rows of 32 bytes whose two pieces change places every four rows, so
+// that eight rows of a piece fall into eight different bank groups.
+constexpr int kTriBytes = 10 * 512;
+__device__ __forceinline__ uint32_t tri_block(int bi, int bj) { return (uint32_t)((bi * (bi + 1) / 2 + bj) * 512); }
+__device__ __forceinline__ uint32_t tri_piece(int r, int pc) { return (uint32_t)(r * 32 + ((pc ^ (r >> 2 & 1)) << 4)); }
 // C fragments of two neighbouring 8-column tiles as the A operand of the 16
 // columns they span, in N parts
 template <int N>
@@ -298,6 +303,46 @@ __device__ __forceinline__ void mma_cols(float (&c0)[4], float (&c1)[4], const u
     mma_parts<NA, NL, KEEP>(c0, c1, a, b);
 }
 
+// B from a 16 x 16 block of packed parts: its rows are n (columns k), or its rows are k (columns n)
+template <int NA, int NB, int KEEP>
+__device__ __forceinline__ void mma_block_rows(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
+                                               uint32_t block)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t b[NB][4];
+#pragma unroll
+    for (int m = 0; m < NB; ++m)
+        ldsm4(block + m * kTriBytes + tri_piece((lane & 7) + (lane >> 4) * 8, lane >> 3 & 1), b[m]);
+    mma_parts<NA, NB, KEEP>(c0, c1, a, b);
+}
+template <int NA, int NB, int KEEP>
+__device__ __forceinline__ void mma_block_cols(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
+                                               uint32_t block)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t b[NB][4];
+#pragma unroll
+    for (int m = 0; m < NB; ++m)
+        ldsm4t(block + m * kTriBytes + tri_piece(lane & 15, lane >> 4), b[m]);
+    mma_parts<NA, NB, KEEP>(c0, c1, a, b);
+}
+// A from a packed block, rows m (columns k), or transposed: rows k (columns m)
+template <int N>
+__device__ __forceinline__ void frag_block(uint32_t block, uint32_t (&a)[N][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        ldsm4(block + n * kTriBytes + tri_piece(lane & 15, lane >> 4), a[n]);
+}
+template <int N>
+__device__ __forceinline__ void frag_block_t(uint32_t block, uint32_t (&a)[N][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        ldsm4t(block + n * kTriBytes + tri_piece((lane & 7) + (lane >> 4) * 8, lane >> 3 & 1), a[n]);
+}
 // A fragment (rows m0.., columns k0..) of a tile stored [k][m] in rows of 128 bytes
 template <int N>
 __device__ __forceinline__ void frag_t(uint32_t tile, int part, int k0, int m0, uint32_t (&a)[N][4])
@@ -306,15 +351,6 @@ __device__ __forceinline__ void frag_t(uint32_t tile, int part, int k0, int m0, 
 #pragma unroll
     for (int n = 0; n < N; ++n)
         ldsm4t(tile + n * part + swz<128>(k0 + (lane & 7) + (lane >> 4) * 8, m0 / 8 + (lane >> 3 & 1)), a[n]);
-}
-// the same of a tile stored [m][k]
-template <int N>
-__device__ __forceinline__ void frag_n(uint32_t tile, int part, int m0, int k0, uint32_t (&a)[N][4])
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        ldsm4(tile + n * part + swz<128>(m0 + (lane & 15), k0 / 8 + (lane >> 4)), a[n]);
 }
 
 // ---- token by token ----------------------------------------------------------
@@ -486,9 +522,8 @@ constexpr int kPrepThreads = 128;
 
 template <int DKP, int NPI, int NPT, int NPP>
 struct PrepLayout {
-    static constexpr int PB = kDeltaC * 128;                   // one part of A, T or P
-    static constexpr int oX = NPT * PB;                        // P, then T; A before it
-    static constexpr int oD = oX + (NPT > NPP ? NPT : NPP) * PB;
+    static constexpr int oX = NPT * kTriBytes;                 // P, then T; A before it
+    static constexpr int oD = oX + (NPT > NPP ? NPT : NPP) * kTriBytes;
     static constexpr int head = oD + 4 * 16 * 20 * 4;          // diagonal blocks of A, rows of 20 floats
     static constexpr int tiles = 2 * NPI * kDeltaC * DKP * 2;  // K and Q, read before the heads
     static constexpr int bytes = tiles > head ? tiles : head;
@@ -622,6 +657,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
     unsigned char *kt = dsm, *qt = dsm + NPI * PB;
     delta_stage_parts<Tin, DKP, NPI>(p, p.k, p.ks, hk, q, t0, kt, kPrepThreads);
     delta_stage_parts<Tin, DKP, NPI>(p, p.q, p.qs, hk, q, t0, qt, kPrepThreads);
+    if (warp == 3)
+        delta_decays(p, q, t0, hk * G, ch, cl, be);
     __syncthreads();
     if (NPI > 1) {   // scratch copies, rows in order (not swizzled)
         const long long base = ((long long)blockIdx.x * p.HK + hk) * NPI * PB;
@@ -644,63 +681,57 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
     delta_rows_product<DKP, NPI, 8>(smem_addr(qt), smem_addr(kt), warp * 16, 0, qk);
     const uint32_t sA = smem_addr(dsm), sX = sA + Lay::oX;
     float *dg = reinterpret_cast<float *>(dsm + Lay::oD);   // [4][16][20]
-    const int r0 = warp * 16 + (lane >> 2);
-    // the lower blocks of N parts from shared memory to a head's part of scratch
-    auto leave = [&](void *dst, int N) {
-        for (int i = tid; i < N * kDeltaC * 8; i += kPrepThreads) {
-            const int r = i >> 3, pc = i & 7, row = r % kDeltaC;   // r counts the parts' rows
-            if (pc / 2 <= row / 16)
-                *reinterpret_cast<uint4 *>(static_cast<char *>(dst) + i * 16) =
-                    *reinterpret_cast<const uint4 *>(dsm + Lay::oX + r / kDeltaC * Lay::PB + swz<128>(row, pc));
-        }
+    const int nb = (min(q.len - t0, kDeltaC) + 15) / 16;    // 16-token blocks that hold tokens
+    // a head's P or T from shared memory to scratch
+    auto leave = [&](void *dst, int bytes) {
+        for (int i = tid; i < bytes / 16; i += kPrepThreads)
+            reinterpret_cast<uint4 *>(dst)[i] = *reinterpret_cast<const uint4 *>(dsm + Lay::oX + i * 16);
     };
     for (int hi = 0; hi < G; ++hi) {
         const int h = hk * G + hi;
         const long long sh = (long long)blockIdx.x * p.H + h;
-        __syncthreads();   // the tiles (or the last head's T) are read
-        if (warp == 0)
-            delta_decays(p, q, t0, h, ch, cl, be);
-        __syncthreads();
+        __syncthreads();   // the tiles (or the last head's T) are read, the decays are here
         if (tid < kDeltaC) {
             float *vec = p.vec + sh * 3 * kDeltaC;
             vec[tid] = expf(ch[tid] + cl[tid]);
             vec[kDeltaC + tid] = expf((ch[kDeltaC - 1] - ch[tid]) + (cl[kDeltaC - 1] - cl[tid]));
             vec[2 * kDeltaC + tid] = be[tid];
         }
+        const int ir = lane >> 2;   // row of the warp's block
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             if (n / 2 > warp)
                 continue;   // above the diagonal blocks
-            const int j0 = n * 8 + (lane & 3) * 2;
+            const int jc = (n & 1) * 8 + (lane & 3) * 2;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const int i = r0 + hf * 8;
+                const int i = warp * 16 + ir + hf * 8;
                 float pv[2], av[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int j = j0 + e;
+                    const int j = n / 2 * 16 + jc + e;
                     const float D = j <= i ? expf((ch[i] - ch[j]) + (cl[i] - cl[j])) : 0.f;
                     pv[e] = j <= i ? p.scale * D * qk[n][hf * 2 + e] : 0.f;
                     av[e] = j < i ? be[i] * D * kk[n][hf * 2 + e] : 0.f;
                 }
-                const uint32_t o = swz<128>(i, n) + (lane & 3) * 4;
+                const uint32_t o = tri_block(warp, n / 2) + tri_piece(ir + hf * 8, n & 1) + (lane & 3) * 4;
                 uint32_t w[NPP], u[NPT];
                 split2<NPP>(pv[0], pv[1], w);
 #pragma unroll
                 for (int m = 0; m < NPP; ++m)
-                    *reinterpret_cast<uint32_t *>(dsm + Lay::oX + m * Lay::PB + o) = w[m];
+                    *reinterpret_cast<uint32_t *>(dsm + Lay::oX + m * kTriBytes + o) = w[m];
                 if (n / 2 < warp) {
                     split2<NPT>(av[0], av[1], u);
 #pragma unroll
                     for (int m = 0; m < NPT; ++m)
-                        *reinterpret_cast<uint32_t *>(dsm + m * Lay::PB + o) = u[m];
+                        *reinterpret_cast<uint32_t *>(dsm + m * kTriBytes + o) = u[m];
                 } else {
-                    *reinterpret_cast<float2 *>(dg + (i * 20 + (j0 & 15))) = make_float2(av[0], av[1]);
+                    *reinterpret_cast<float2 *>(dg + (i * 20 + jc)) = make_float2(av[0], av[1]);
                 }
             }
         }
         __syncthreads();
-        leave(static_cast<char *>(p.Pp) + sh * NPP * Lay::PB, NPP);
+        leave(static_cast<char *>(p.Pp) + sh * NPP * kTriBytes, NPP * kTriBytes);
         // column j = lane of the diagonal block's inverse
         float col[16];
         if (lane < 16) {
@@ -727,26 +758,30 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float x = col[i];
-                unsigned char *o = dsm + Lay::oX + swz<128>(warp * 16 + i, warp * 2 + (lane >> 3)) + (lane & 7) * 2;
+                unsigned char *o = dsm + Lay::oX + tri_block(warp, warp) + tri_piece(i, lane >> 3) + (lane & 7) * 2;
 #pragma unroll
                 for (int m = 0; m < NPT; ++m) {
                     const __nv_bfloat16 b = __float2bfloat16_rn(x);
-                    *reinterpret_cast<__nv_bfloat16 *>(o + m * Lay::PB) = b;
+                    *reinterpret_cast<__nv_bfloat16 *>(o + m * kTriBytes) = b;
                     x -= __bfloat162float(b);
                 }
             }
         }
         __syncthreads();
+        if (warp == 3 && hi + 1 < G)   // the next head's decays, by the warp that has no column of blocks
+            delta_decays(p, q, t0, h + 1, ch, cl, be);
         for (int i = warp + 1; i < 4; ++i) {
             float w0[4] = {0.f, 0.f, 0.f, 0.f}, w1[4] = {0.f, 0.f, 0.f, 0.f}, u0[4] = {0.f, 0.f, 0.f, 0.f},
                   u1[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t a[NPT][4];
-            for (int m = warp; m < i; ++m) {
-                frag_t<NPT>(sX, Lay::PB, m * 16, warp * 16, a);
-                mma_rows<128, NPT, NPT, NPT>(w0, w1, a, sA, Lay::PB, i * 16, m * 2);
+            if (i < nb) {   // blocks of no token have A = 0, and T = 0
+                for (int m = warp; m < i; ++m) {
+                    frag_block_t<NPT>(sX + tri_block(m, warp), a);
+                    mma_block_rows<NPT, NPT, NPT>(w0, w1, a, sA + tri_block(i, m));
+                }
+                frag_a<NPT>(w0, w1, a);
+                mma_block_rows<NPT, NPT, NPT>(u0, u1, a, sX + tri_block(i, i));
             }
-            frag_a<NPT>(w0, w1, a);
-            mma_rows<128, NPT, NPT, NPT>(u0, u1, a, sX, Lay::PB, i * 16, i * 2);
             uint32_t o[4][NPT];
             split2<NPT>(-u0[0], -u0[1], o[0]);
             split2<NPT>(-u0[2], -u0[3], o[1]);
@@ -755,13 +790,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
 #pragma unroll
             for (int m = 0; m < NPT; ++m) {
                 const uint32_t r[4] = {o[0][m], o[1][m], o[2][m], o[3][m]};
-                stsm4t(sX + m * Lay::PB + swz<128>(i * 16 + (lane & 7) + (lane >> 4) * 8, warp * 2 + (lane >> 3 & 1)),
+                stsm4t(sX + m * kTriBytes + tri_block(i, warp) +
+                           tri_piece((lane & 7) + (lane >> 4) * 8, lane >> 3 & 1),
                        r);
             }
             __syncwarp();
         }
         __syncthreads();
-        leave(static_cast<char *>(p.Tp) + sh * NPT * Lay::PB, NPT);
+        leave(static_cast<char *>(p.Tp) + sh * NPT * kTriBytes, NPT * kTriBytes);
     }
 }
 

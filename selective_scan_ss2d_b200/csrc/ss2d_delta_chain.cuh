@@ -9,13 +9,13 @@
 // have as A operand what the warp just computed (an accumulator fragment,
 // split into bf16 parts, is an A fragment lane by lane) and as B operand K, Q,
 // T or P from shared memory, by rows or by columns.  No value passes between
-// warps, and a chunk needs one barrier, for the stage of shared memory that
-// the next chunk is copied into meanwhile.  The reverse pass has the same
-// shape:
+// warps, and a chunk needs one barrier for its stage of shared memory.  The
+// reverse pass has the same shape:
 //     dV'^T = dO^T P + e^{c_last - c} (dS^T K^T),  dX^T = dV'^T T,  dR = -beta e^c dX,
 //     dS^T <- e^{c_last} dS^T + (scale e^c dO)^T Q + dR^T K
-// T and P are lower triangular in 16 x 16 blocks: the blocks above the
-// diagonal are neither copied nor multiplied.
+// It needs nothing of the forward chain, so that a backward pass runs both in
+// one launch.  Blocks of 16 tokens behind a sequence's end are left out of
+// every product: 197 tokens are 13 blocks, not four chunks of four.
 #pragma once
 
 #include "ss2d_delta.cuh"
@@ -24,39 +24,38 @@ namespace ss2d {
 
 enum { kChainOut = 0, kChainState = 1, kChainRev = 2 };
 
-template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP>
+template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP, int STAGES>
 struct ChainLayout {
     static constexpr int NPI = DeltaParts<Tin>::n;
     static constexpr int DVT = NW * 16;
     static constexpr int KB = NPI * kDeltaC * DKP * 2;           // K; Q the same
-    static constexpr int TB = kDeltaC * kDeltaC * 2;             // one part of T or P
     static constexpr int VRB = sizeof(Tin) == 2 ? DVT * 2 : (DVT + 4) * 4;   // row of V or dO
     static constexpr int oK = 0;
     static constexpr int oQ = KB;
-    static constexpr int oT = MODE == kChainState ? oQ : oQ + KB;
-    static constexpr int oP = oT + NP * TB;
-    static constexpr int oV = MODE == kChainState ? oP : oP + NPP * TB;
-    static constexpr int oX = oV + kDeltaC * VRB;                // e^c, e^{c_last - c}, beta
+    static constexpr int oV = MODE == kChainState ? oQ : oQ + KB;
+    static constexpr int oT = oV + kDeltaC * VRB;
+    static constexpr int oP = oT + NP * kTriBytes;
+    static constexpr int oX = MODE == kChainState ? oP : oP + NPP * kTriBytes;   // e^c, e^{c_last - c}, beta
     static constexpr int stage = (oX + 3 * kDeltaC * 4 + 127) / 128 * 128;
     static constexpr int out = sizeof(Tin) == 2 && MODE != kChainState ? NW * kDeltaC * 32 : 0;
-    static constexpr int stages = 2 * stage + out <= 225 * 1024 ? 2 : 1;
-    static constexpr int bytes = stages * stage + out;
+    static constexpr int bytes = STAGES * stage + out;
 };
 
-// NP parts of intermediate values (states, X, V'), NPP of P and of what only the output is made of
-template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP>
-__global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaParams p)
+// NP parts of intermediate values (states, X, V'), NPP of P and of what only the
+// output is made of.  tile, seq0, seqs: the block's DV tile, first sequence and stride
+template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP, int STAGES>
+__device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int seq0, int seqs)
 {
-    using Lay = ChainLayout<Tin, DKP, NW, MODE, NP, NPP>;
+    using Lay = ChainLayout<Tin, DKP, NW, MODE, NP, NPP, STAGES>;
     constexpr int NPI = Lay::NPI, NT = NW * 32, RBK = DKP * 2, PBK = kDeltaC * RBK, NK = DKP / 8;
     extern __shared__ __align__(128) unsigned char dsm[];
     const uint32_t sm0 = smem_addr(dsm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, t2 = (lane & 3) * 2;   // row and first column of a lane in an accumulator tile
     const int h = blockIdx.y, hk = h / (p.H / p.HK);
-    const int dvw = (blockIdx.x * NW + warp) * 16;   // first of the warp's DV columns
+    const int dvw = (tile * NW + warp) * 16;   // first of the warp's DV columns
     const bool won = dvw < p.DV;
-    for (int sn = blockIdx.z; sn < p.nseq; sn += gridDim.z) {
+    for (int sn = seq0; sn < p.nseq; sn += seqs) {
         const DeltaSeq q = delta_seq(p, sn);
         const int nc = (q.len + kDeltaC - 1) / kDeltaC;
         const long long slot0 = delta_slot0(p, sn, q);
@@ -87,24 +86,15 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
                 if constexpr (MODE != kChainState)
                     cp16(dst + Lay::oQ, qs, on);
             }
-            for (int i = tid; i < kDeltaC * 8; i += NT) {
-                const int r = i >> 3, pc = i & 7;
-                if (pc / 2 > r / 16)
-                    continue;
-#pragma unroll
-                for (int m = 0; m < NP; ++m)
-                    cp16(base + Lay::oT + m * Lay::TB + swz<128>(r, pc),
-                         static_cast<const char *>(p.Tp) + (sh * NP + m) * Lay::TB + i * 16, true);
-                if constexpr (MODE != kChainState) {
-#pragma unroll
-                    for (int m = 0; m < NPP; ++m)
-                        cp16(base + Lay::oP + m * Lay::TB + swz<128>(r, pc),
-                             static_cast<const char *>(p.Pp) + (sh * NPP + m) * Lay::TB + i * 16, true);
-                }
-            }
+            for (int i = tid; i < NP * kTriBytes / 16; i += NT)
+                cp16(base + Lay::oT + i * 16, static_cast<const char *>(p.Tp) + sh * NP * kTriBytes + i * 16, true);
+            if constexpr (MODE != kChainState)
+                for (int i = tid; i < NPP * kTriBytes / 16; i += NT)
+                    cp16(base + Lay::oP + i * 16, static_cast<const char *>(p.Pp) + sh * NPP * kTriBytes + i * 16,
+                         true);
             constexpr int VPC = Lay::DVT * (int)sizeof(Tin) / 16, VPE = 16 / (int)sizeof(Tin);
             for (int i = tid; i < kDeltaC * VPC; i += NT) {
-                const int r = i / VPC, pc = i % VPC, d = blockIdx.x * Lay::DVT + pc * VPE;
+                const int r = i / VPC, pc = i % VPC, d = tile * Lay::DVT + pc * VPE;
                 const bool on = t0 + r < q.len && d < p.DV;
                 const long long tok = delta_token(p, q, on ? t0 + r : 0);
                 const Tin *src = MODE == kChainRev ? static_cast<const Tin *>(p.dout) + (tok * p.H + h) * p.DV
@@ -116,34 +106,33 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
                 cp16(base + Lay::oX + tid * 16, p.vec + sh * 3 * kDeltaC + tid * 4, true);
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         };
-        // V or dO of the warp's columns, transposed, in accumulator layout
-        auto values = [&](const unsigned char *base, float (&v)[8][4]) {
+        // V or dO of the warp's columns and 16 tokens, transposed, in accumulator layout
+        auto values = [&](const unsigned char *base, int blk, float (&v0)[4], float (&v1)[4]) {
             if constexpr (sizeof(Tin) == 2) {
+                uint32_t r[4];
+                ldsm4t(smem_addr(base) + Lay::oV +
+                           swz<Lay::DVT * 2>(blk * 16 + (lane & 7) + (lane >> 4) * 8, warp * 2 + (lane >> 3 & 1)),
+                       r);
 #pragma unroll
-                for (int nt = 0; nt < 8; nt += 2) {
-                    uint32_t r[4];
-                    ldsm4t(smem_addr(base) + Lay::oV +
-                               swz<Lay::DVT * 2>(nt * 8 + (lane & 7) + (lane >> 4) * 8, warp * 2 + (lane >> 3 & 1)),
-                           r);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[nt + (j >> 1)][(j & 1) * 2] = half_bits_to_f32<Tin>(r[j] & 0xffffu);
-                        v[nt + (j >> 1)][(j & 1) * 2 + 1] = half_bits_to_f32<Tin>(r[j] >> 16);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    v0[j * 2] = half_bits_to_f32<Tin>(r[j] & 0xffffu);
+                    v0[j * 2 + 1] = half_bits_to_f32<Tin>(r[j] >> 16);
+                    v1[j * 2] = half_bits_to_f32<Tin>(r[2 + j] & 0xffffu);
+                    v1[j * 2 + 1] = half_bits_to_f32<Tin>(r[2 + j] >> 16);
                 }
             } else {
                 const float *vt = reinterpret_cast<const float *>(base + Lay::oV) + warp * 16;
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[nt][j] = vt[(nt * 8 + t2 + (j & 1)) * (Lay::DVT + 4) + g8 + (j >> 1) * 8];
+                for (int j = 0; j < 4; ++j) {
+                    v0[j] = vt[(blk * 16 + t2 + (j & 1)) * (Lay::DVT + 4) + g8 + (j >> 1) * 8];
+                    v1[j] = vt[(blk * 16 + 8 + t2 + (j & 1)) * (Lay::DVT + 4) + g8 + (j >> 1) * 8];
+                }
             }
         };
         // a 16 x 64 result, transposed back and rounded, into the rows of a (tokens, H, DV) tensor
         auto emit = [&](const float (&v)[8][4], void *dst, int t0) {
             if constexpr (sizeof(Tin) == 2) {
-                const uint32_t ob = sm0 + Lay::stages * Lay::stage + warp * kDeltaC * 32;
+                const uint32_t ob = sm0 + STAGES * Lay::stage + warp * kDeltaC * 32;
 #pragma unroll
                 for (int nt = 0; nt < 8; nt += 2) {
                     uint32_t r[4];
@@ -164,7 +153,7 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
                 for (int i = lane; i < kDeltaC * 2; i += 32) {
                     const int t = t0 + (i >> 1);
                     if (won && t < q.len) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(dsm + Lay::stages * Lay::stage +
+                        const uint4 u = *reinterpret_cast<const uint4 *>(dsm + STAGES * Lay::stage +
                                                                          warp * kDeltaC * 32 + i * 16);
                         *reinterpret_cast<uint4 *>(static_cast<Tin *>(dst) +
                                                    (delta_token(p, q, t) * p.H + h) * p.DV + dvw + (i & 1) * 8) = u;
@@ -206,16 +195,16 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
         if (nc > 0)
             load(chunk(0), 0);
         for (int i = 0; i < nc; ++i) {
-            const int c = chunk(i), st = Lay::stages == 2 ? i & 1 : 0, t0 = c * kDeltaC;
+            const int c = chunk(i), st = STAGES == 2 ? i & 1 : 0, t0 = c * kDeltaC;
             const long long sh = (slot0 + c) * p.H + h;
             asm volatile("cp.async.wait_group 0;\n" ::: "memory");
             __syncthreads();   // the stage is here, and every warp is done with the other one
-            if (Lay::stages == 2 && i + 1 < nc)
+            if (STAGES == 2 && i + 1 < nc)
                 load(chunk(i + 1), st ^ 1);
             const unsigned char *sb = dsm + st * Lay::stage;
             const uint32_t sa = sm0 + st * Lay::stage;
             const float *eg = reinterpret_cast<const float *>(sb + Lay::oX), *el = eg + kDeltaC, *be = el + kDeltaC;
-            const float elast = eg[kDeltaC - 1];
+            const int nb = (min(q.len - t0, kDeltaC) + 15) / 16;   // blocks of 16 tokens that hold tokens
             if (won) {
                 if constexpr (MODE != kChainOut) {
                     float *dst = MODE == kChainRev ? p.dSx : p.Sx;
@@ -229,44 +218,68 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         R[n][j] = O[n][j] = 0.f;
-                // (K S)^T, and (Q S)^T for the output
+                // (K S)^T
 #pragma unroll
                 for (int ks = 0; ks < DKP / 16; ++ks) {
                     uint32_t a[NP][4];
                     frag_a<NP>(S[2 * ks], S[2 * ks + 1], a);
 #pragma unroll
-                    for (int nt = 0; nt < 8; nt += 2) {
-                        mma_rows<RBK, NP, NPI, NP>(R[nt], R[nt + 1], a, sa + Lay::oK, PBK, nt * 8, ks * 2);
-                        if constexpr (MODE == kChainOut)
-                            mma_rows<RBK, NP, NPI, NPP>(O[nt], O[nt + 1], a, sa + Lay::oQ, PBK, nt * 8, ks * 2);
-                    }
+                    for (int b = 0; b < 4; ++b)
+                        if (b < nb)
+                            mma_rows<RBK, NP, NPI, NP>(R[2 * b], R[2 * b + 1], a, sa + Lay::oK, PBK, b * 16, ks * 2);
                 }
-                float V[8][4];
                 if constexpr (MODE != kChainRev) {
-                    values(sb, V);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) {
+                    for (int b = 0; b < 4; ++b) {
+                        if (b < nb) {
+                            float v[2][4];
+                            values(sb, b, v[0], v[1]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            V[n][j] -= eg[n * 8 + t2 + (j & 1)] * R[n][j];   // Y
-                        if constexpr (MODE == kChainState)
-                            put(p.Yx, sh, kDeltaC, n, V[n]);
+                            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            V[n][j] *= be[n * 8 + t2 + (j & 1)];             // X
-                            R[n][j] = 0.f;
+                                for (int j = 0; j < 4; ++j)
+                                    R[2 * b + e][j] = v[e][j] - eg[b * 16 + e * 8 + t2 + (j & 1)] * R[2 * b + e][j];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if constexpr (MODE == kChainState)
+                                put(p.Yx, sh, kDeltaC, 2 * b + e, R[2 * b + e]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                R[2 * b + e][j] *= be[b * 16 + e * 8 + t2 + (j & 1)];   // X
                         }
                     }
                     // V'^T = X^T T^T
+                    float W[8][4];
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            W[n][j] = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
+                        if (ks >= nb)
+                            continue;
                         uint32_t a[NP][4];
-                        frag_a<NP>(V[2 * ks], V[2 * ks + 1], a);
+                        frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
 #pragma unroll
-                        for (int nt = 2 * ks; nt < 8; nt += 2)
-                            mma_rows<128, NP, NP, NP>(R[nt], R[nt + 1], a, sa + Lay::oT, Lay::TB, nt * 8, ks * 2);
+                        for (int b = ks; b < 4; ++b)
+                            if (b < nb)
+                                mma_block_rows<NP, NP, NP>(W[2 * b], W[2 * b + 1], a,
+                                                           sa + Lay::oT + tri_block(b, ks));
                     }
                     if constexpr (MODE == kChainOut) {
+                        // O^T = scale e^c (Q S)^T + V'^T P^T
+#pragma unroll
+                        for (int ks = 0; ks < DKP / 16; ++ks) {
+                            uint32_t a[NPP][4];
+                            frag_a<NPP>(S[2 * ks], S[2 * ks + 1], a);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (b < nb)
+                                    mma_rows<RBK, NPP, NPI, NPP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oQ, PBK, b * 16,
+                                                                 ks * 2);
+                        }
 #pragma unroll
                         for (int n = 0; n < 8; ++n)
 #pragma unroll
@@ -274,70 +287,57 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
                                 O[n][j] *= p.scale * eg[n * 8 + t2 + (j & 1)];
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
+                            if (ks >= nb)
+                                continue;
                             uint32_t a[NPP][4];
-                            frag_a<NPP>(R[2 * ks], R[2 * ks + 1], a);
+                            frag_a<NPP>(W[2 * ks], W[2 * ks + 1], a);
 #pragma unroll
-                            for (int nt = 2 * ks; nt < 8; nt += 2)
-                                mma_rows<128, NPP, NPP, NPP>(O[nt], O[nt + 1], a, sa + Lay::oP, Lay::TB, nt * 8,
-                                                             ks * 2);
+                            for (int b = ks; b < 4; ++b)
+                                if (b < nb)
+                                    mma_block_rows<NPP, NPP, NPP>(O[2 * b], O[2 * b + 1], a,
+                                                                  sa + Lay::oP + tri_block(b, ks));
                         }
                         emit(O, p.o, t0);
                     } else {
 #pragma unroll
                         for (int n = 0; n < 8; ++n)
-                            put(p.Vx, sh, kDeltaC, n, R[n]);
+                            put(p.Vx, sh, kDeltaC, n, W[n]);
                     }
-                    // S^T <- e^{c_last} S^T + (e^{c_last - c} V')^T K
 #pragma unroll
                     for (int n = 0; n < 8; ++n)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            R[n][j] *= el[n * 8 + t2 + (j & 1)];
+                            R[n][j] = W[n][j] * el[n * 8 + t2 + (j & 1)];
                 } else {
-                    // R = (K dS)^T: its product with V' goes to the gradient of the decays
-                    float kl[8][2];
-                    const float *vx = p.Vx + (sh * p.DV + dvw + g8) * kDeltaC + t2;
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        const float2 v0 = *reinterpret_cast<const float2 *>(vx + n * 8);
-                        const float2 v1 = *reinterpret_cast<const float2 *>(vx + 8 * kDeltaC + n * 8);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            R[n][j] *= el[n * 8 + t2 + (j & 1)];
-                        kl[n][0] = fmaf(R[n][0], v0.x, R[n][2] * v1.x);
-                        kl[n][1] = fmaf(R[n][1], v0.y, R[n][3] * v1.y);
-                    }
+                    // dV'^T = dO^T P + e^{c_last - c} (K dS)^T: row i of P holds its columns j <= i
 #pragma unroll
                     for (int n = 0; n < 8; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            for (int m = 4; m < 32; m <<= 1)
-                                kl[n][e] += __shfl_xor_sync(0xffffffffu, kl[n][e], m);
-                        }
-                    if (g8 == 0) {
-                        float *dst = p.klx + (sh * (p.DV / 16) + dvw / 16) * kDeltaC + t2;
-#pragma unroll
-                        for (int n = 0; n < 8; ++n)
-                            *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(kl[n][0], kl[n][1]);
-                    }
-                    // dV'^T = dO^T P + e^{c_last - c} (K dS)^T: row i of P holds its columns j <= i
-                    values(sb, V);
+                        for (int j = 0; j < 4; ++j)
+                            R[n][j] *= el[n * 8 + t2 + (j & 1)];
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
+                        if (ks >= nb)
+                            continue;
+                        float v[2][4];
+                        values(sb, ks, v[0], v[1]);
                         uint32_t a[NPI][4];
-                        frag_a<NPI>(V[2 * ks], V[2 * ks + 1], a);
+                        frag_a<NPI>(v[0], v[1], a);
 #pragma unroll
-                        for (int nt = 0; nt <= 2 * ks; nt += 2)
-                            mma_cols<128, NPI, NPP, NPP>(R[nt], R[nt + 1], a, sa + Lay::oP, Lay::TB, ks * 16, nt);
+                        for (int b = 0; b <= ks; ++b)
+                            mma_block_cols<NPI, NPP, NPP>(R[2 * b], R[2 * b + 1], a,
+                                                          sa + Lay::oP + tri_block(ks, b));
                     }
                     // dX^T = dV'^T T
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
+                        if (ks >= nb)
+                            continue;
                         uint32_t a[NP][4];
                         frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
 #pragma unroll
-                        for (int nt = 0; nt <= 2 * ks; nt += 2)
-                            mma_cols<128, NP, NP, NP>(O[nt], O[nt + 1], a, sa + Lay::oT, Lay::TB, ks * 16, nt);
+                        for (int b = 0; b <= ks; ++b)
+                            mma_block_cols<NP, NP, NP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oT + tri_block(ks, b));
                     }
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
@@ -346,11 +346,12 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
                         for (int j = 0; j < 4; ++j) {
                             O[n][j] *= be[n * 8 + t2 + (j & 1)];
                             R[n][j] = -eg[n * 8 + t2 + (j & 1)] * O[n][j];   // dR
-                            V[n][j] *= p.scale * eg[n * 8 + t2 + (j & 1)];
                         }
                     }
                     emit(O, p.dv, t0);
                 }
+                // S^T <- e^{c_last} S^T + (e^{c_last - c} V')^T K, or dR^T K + (scale e^c dO)^T Q
+                const float elast = eg[kDeltaC - 1];
 #pragma unroll
                 for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -358,20 +359,29 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
                         S[n][j] *= elast;
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
+                    if (ks >= nb)
+                        continue;
                     uint32_t a[NP][4];
                     frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
 #pragma unroll
                     for (int nt = 0; nt < NK; nt += 2)
                         mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oK, PBK, ks * 16, nt);
                     if constexpr (MODE == kChainRev) {
-                        frag_a<NP>(V[2 * ks], V[2 * ks + 1], a);
+                        float v[2][4];
+                        values(sb, ks, v[0], v[1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[e][j] *= p.scale * eg[ks * 16 + e * 8 + t2 + (j & 1)];
+                        frag_a<NP>(v[0], v[1], a);
 #pragma unroll
                         for (int nt = 0; nt < NK; nt += 2)
                             mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, nt);
                     }
                 }
             }
-            if (Lay::stages == 1 && i + 1 < nc) {
+            if (STAGES == 1 && i + 1 < nc) {
                 __syncthreads();
                 load(chunk(i + 1), 0);
             }
@@ -389,6 +399,30 @@ __global__ void __launch_bounds__(NW * 32, 1) delta_chain_kernel(const DeltaPara
         }
         __syncthreads();
     }
+}
+
+// CTAs per SM that the registers are held to: three of four warps where three stages of shared memory fit
+template <typename Lay, int DKP, int STAGES>
+constexpr int chain_ctas() { return STAGES == 1 && DKP == 64 && Lay::bytes <= 74 * 1024 ? 3 : 2; }
+
+template <typename Tin, int DKP, int NW, int NP, int NPP, int STAGES>
+__global__ void
+    __launch_bounds__(NW * 32,
+                      (chain_ctas<ChainLayout<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>, DKP, STAGES>()))
+        delta_out_kernel(const DeltaParams p)
+{
+    delta_chain<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>(p, blockIdx.x, blockIdx.z, gridDim.z);
+}
+// the forward chain and the reverse one, the longer one first
+template <typename Tin, int DKP, int NW, int STAGES>
+__global__ void __launch_bounds__(NW * 32,
+                                  (chain_ctas<ChainLayout<Tin, DKP, NW, kChainRev, 3, 3, STAGES>, DKP, STAGES>()))
+    delta_both_kernel(const DeltaParams p)
+{
+    if (blockIdx.x & 1)
+        delta_chain<Tin, DKP, NW, kChainState, 3, 3, STAGES>(p, blockIdx.x >> 1, blockIdx.z, gridDim.z);
+    else
+        delta_chain<Tin, DKP, NW, kChainRev, 3, 3, STAGES>(p, blockIdx.x >> 1, blockIdx.z, gridDim.z);
 }
 
 }  // namespace ss2d

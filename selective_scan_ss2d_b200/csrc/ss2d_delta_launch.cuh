@@ -27,11 +27,11 @@ cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP>
-cudaError_t launch_chain_nw(const DeltaParams &p, cudaStream_t st)
+template <typename Tin, int DKP, int NW, int NP, int NPP, int STAGES>
+cudaError_t launch_out(const DeltaParams &p, cudaStream_t st)
 {
-    constexpr int smem = ChainLayout<Tin, DKP, NW, MODE, NP, NPP>::bytes;
-    auto kern = delta_chain_kernel<Tin, DKP, NW, MODE, NP, NPP>;
+    constexpr int smem = ChainLayout<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>::bytes;
+    auto kern = delta_out_kernel<Tin, DKP, NW, NP, NPP, STAGES>;
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
@@ -39,17 +39,54 @@ cudaError_t launch_chain_nw(const DeltaParams &p, cudaStream_t st)
     kern<<<grid, NW * 32, smem, st>>>(p);
     return cudaGetLastError();
 }
-
-// Eight warps (128 columns of DV) share a chunk's K, Q, T and P when there
-// are enough such CTAs for every SM; otherwise four warps, one per scheduler,
-// on twice as many SMs.
-template <typename Tin, int DKP, int MODE, int NP, int NPP>
-cudaError_t launch_chain(const DeltaParams &p, cudaStream_t st)
+template <typename Tin, int DKP, int NW, int STAGES>
+cudaError_t launch_both(const DeltaParams &p, cudaStream_t st)
 {
-    const long long wide = (long long)((p.DV + 127) / 128) * p.H * p.nseq;
-    if (p.DV > 64 && wide >= 148)
-        return launch_chain_nw<Tin, DKP, 8, MODE, NP, NPP>(p, st);
-    return launch_chain_nw<Tin, DKP, 4, MODE, NP, NPP>(p, st);
+    constexpr int smem = ChainLayout<Tin, DKP, NW, kChainRev, 3, 3, STAGES>::bytes;
+    auto kern = delta_both_kernel<Tin, DKP, NW, STAGES>;
+    const cudaError_t e = delta_smem(kern, smem);
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid(2 * ((p.DV + NW * 16 - 1) / (NW * 16)), p.H, p.nseq < 65535 ? p.nseq : 65535);
+    kern<<<grid, NW * 32, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+// Stages that fit: a second one hides the next chunk's copies behind this chunk's
+// products; one leaves room for a second and third CTA, which hide them too.
+constexpr int chain_stages(int two_bytes) { return two_bytes <= 225 * 1024 ? 2 : 1; }
+
+// CTAs of four warps (64 columns of DV).  With more of them than two per SM, a
+// single stage and up to three CTAs per SM; otherwise two stages if they fit.
+template <typename Tin, int DKP, int NP, int NPP>
+cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
+{
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * p.nseq;
+    constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainOut, NP, NPP, 2>::bytes);
+    if (two == 1 || ctas > 2 * 148)
+        return launch_out<Tin, DKP, 4, NP, NPP, 1>(p, st);
+    return launch_out<Tin, DKP, 4, NP, NPP, two>(p, st);
+}
+template <typename Tin, int DKP>
+cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
+{
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * p.nseq * 2;
+    constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainRev, 3, 3, 2>::bytes);
+    if (two == 1 || ctas > 2 * 148)
+        return launch_both<Tin, DKP, 4, 1>(p, st);
+    return launch_both<Tin, DKP, 4, two>(p, st);
+}
+
+template <typename Tin, int DKP, bool SHARED>
+cudaError_t launch_grad(const DeltaParams &p, cudaStream_t st)
+{
+    constexpr int smem = GradLayout<Tin, DKP>::bytes;
+    auto kern = delta_grad_kernel<Tin, DKP, SHARED>;
+    const cudaError_t e = delta_smem(kern, smem);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<dim3((unsigned)p.nslots, p.HK), kGradThreads, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename Tin, int DKP>
@@ -57,18 +94,10 @@ cudaError_t launch_bwd(const DeltaParams &p, cudaStream_t st)
 {
     cudaError_t e = launch_prep<Tin, DKP, 3, 3>(p, st);
     if (e == cudaSuccess)
-        e = launch_chain<Tin, DKP, kChainState, 3, 3>(p, st);
-    if (e == cudaSuccess)
-        e = launch_chain<Tin, DKP, kChainRev, 3, 3>(p, st);
+        e = launch_chain_both<Tin, DKP>(p, st);
     if (e != cudaSuccess)
         return e;
-    constexpr int smem = GradLayout<Tin, DKP>::bytes;
-    auto kern = delta_grad_kernel<Tin, DKP>;
-    e = delta_smem(kern, smem);
-    if (e != cudaSuccess)
-        return e;
-    kern<<<dim3((unsigned)p.nslots, p.HK), kGradThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return p.H > p.HK ? launch_grad<Tin, DKP, true>(p, st) : launch_grad<Tin, DKP, false>(p, st);
 }
 
 template <typename Tin, int DKP>
@@ -77,14 +106,14 @@ cudaError_t launch_fwd(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t s
     cudaError_t e;
     if constexpr (sizeof(Tin) == 4) {
         e = launch_prep<Tin, DKP, 3, 3>(p, st);
-        return e != cudaSuccess ? e : launch_chain<Tin, DKP, kChainOut, 3, 3>(p, st);
+        return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, 3, 3>(p, st);
     } else {
         if (pl.np == 3) {
             e = launch_prep<Tin, DKP, 3, 2>(p, st);
-            return e != cudaSuccess ? e : launch_chain<Tin, DKP, kChainOut, 3, 2>(p, st);
+            return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, 3, 2>(p, st);
         }
         e = launch_prep<Tin, DKP, 2, 2>(p, st);
-        return e != cudaSuccess ? e : launch_chain<Tin, DKP, kChainOut, 2, 2>(p, st);
+        return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, 2, 2>(p, st);
     }
 }
 

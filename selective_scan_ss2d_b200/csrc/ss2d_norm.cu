@@ -91,7 +91,10 @@ cudaError_t launch(const NormCall &c, bool bwd, int grid, int threads, cudaStrea
 {
     if (bwd) {
         const size_t smem = sizeof(float) * threads * E;
-        ss2d::norm_bwd_kernel<Tin, Tr, V, E><<<grid, threads, smem, st>>>(c.p);
+        if (c.p.cols >> 3)
+            ss2d::norm_bwd_kernel<Tin, Tr, V, E, true><<<grid, threads, smem, st>>>(c.p);
+        else
+            ss2d::norm_bwd_kernel<Tin, Tr, V, E, false><<<grid, threads, smem, st>>>(c.p);
     } else {
         ss2d::norm_fwd_kernel<Tin, Tr, V, E><<<grid, threads, 0, st>>>(c.p);
     }
@@ -167,7 +170,8 @@ int block_norm_fwd(const void *x, const void *z, const void *r, const float *s, 
     p.tpr = team_size(D, D <= 4096 ? 8 : 16);
     const int threads = p.tpr > 256 ? p.tpr : 256;
     const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
-    const int grid = ctas > (1 << 30) ? 1 << 30 : (int)ctas;
+    // four CTAs of 256 threads at the kernel's registers fill an SM
+    const int grid = ctas > 148 * 4 ? 148 * 4 : (int)ctas;
     const cudaError_t e = launch_norm(c, false, grid, threads, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
         ss2d::record_error("kernel launch", e);
@@ -210,7 +214,7 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
     if (rc != SS2D_OK || D == 0)
         return rc;
     // column sums of a part that the call does not have are not written
-    const ss2d::NormSums out{{ds, post ? dw_post : nullptr, post ? db_post : nullptr, pre ? dw_pre : nullptr,
+    const ss2d::NormSums out{{ds, post ? dw_post : nullptr, pre ? dw_pre : nullptr, post ? db_post : nullptr,
                               pre ? db_pre : nullptr}};
     for (int i = 0; i < ss2d::kNormCols; ++i)
         p.cols |= (out.out[i] ? 1 : 0) << i;
@@ -250,7 +254,7 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
     p.part = static_cast<float *>(part);
     e = launch_norm(c, true, grid, threads, st);
     if (e == cudaSuccess && p.cols) {
-        ss2d::norm_colsum_kernel<<<dim3((D + 31) / 32, ss2d::kNormCols), 256, 0, st>>>(p.part, out, grid, D);
+        ss2d::norm_colsum_kernel<<<dim3((D + 31) / 32, ss2d::kNormCols), 1024, 0, st>>>(p.part, out, grid, D);
         e = cudaGetLastError();
     }
     cudaError_t ef = cudaSuccess;

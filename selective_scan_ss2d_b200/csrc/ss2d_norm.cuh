@@ -40,7 +40,7 @@
 namespace ss2d {
 
 enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
-constexpr int kNormCols = 5;   // ds, dw_post, db_post, dw_pre, db_pre
+constexpr int kNormCols = 5;   // ds, dw_post, dw_pre, db_post, db_pre
 
 struct NormParams {
     const void *x, *z, *r;   // r: the residual (forward), r' as the forward stored it (backward)
@@ -56,32 +56,83 @@ struct NormParams {
     float eps;
 };
 
-// E values of one row: thread t of a team holds vectors t, t + TPR, ... of V values
+// Thread t of a team holds vectors t, t + TPR, ... of V values of a row; a
+// vector is 16 bytes of 16-bit values, two 16-byte pieces of float32, or (V = 1)
+// one value.  Rows are loaded as stored and converted when they are used, so that
+// the next row can be on its way at half the registers.
+template <typename T, int V>
+struct NormVec {
+    static constexpr int n = V == 1 ? 1 : V * (int)sizeof(T) / 16;
+    typename std::conditional<V == 1, T, uint4>::type w[n];
+    __device__ __forceinline__ void load(const T *row, int col)
+    {
+        if constexpr (V == 1) {
+            w[0] = row[col];
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                w[i] = reinterpret_cast<const uint4 *>(row + col)[i];
+        }
+    }
+    __device__ __forceinline__ void zero()
+    {
+        if constexpr (V == 1) {
+            w[0] = T(0.f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                w[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void get(float *v) const
+    {
+        if constexpr (V == 1) {
+            v[0] = to_f32(w[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 4) {
+                        v[4 * i + j] = __uint_as_float(u[j]);
+                    } else {
+                        v[8 * i + 2 * j] = half_bits_to_f32<T>(u[j] & 0xffffu);
+                        v[8 * i + 2 * j + 1] = half_bits_to_f32<T>(u[j] >> 16);
+                    }
+                }
+            }
+        }
+    }
+};
 template <typename T, int V>
 __device__ __forceinline__ void norm_load(const T *row, int col, float *v)
 {
-    if constexpr (V == 1) {
-        v[0] = to_f32(row[col]);
-    } else if constexpr (sizeof(T) == 4) {
+    NormVec<T, V> r;
+    r.load(row, col);
+    r.get(v);
+}
+// a row's vectors, zero past its end and for rows past the last
+template <typename T, int V, int E>
+struct NormRow {
+    NormVec<T, V> v[E / V];
+    template <typename Col>
+    __device__ __forceinline__ void load(const T *row, bool live, int D, Col col)
+    {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(row + col + i);
-            v[i] = f.x;
-            v[i + 1] = f.y;
-            v[i + 2] = f.z;
-            v[i + 3] = f.w;
-        }
-    } else {
-        static_assert(V % 8 == 0, "16-byte vectors");
-        const uint4 u = *reinterpret_cast<const uint4 *>(row + col);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = half_bits_to_f32<T>(w[i] & 0xffffu);
-            v[2 * i + 1] = half_bits_to_f32<T>(w[i] >> 16);
+        for (int i = 0; i < E / V; ++i) {
+            v[i].zero();
+            if (live && col(i) < D)
+                v[i].load(row, col(i));
         }
     }
-}
+    __device__ __forceinline__ void get(float (&f)[E]) const
+    {
+#pragma unroll
+        for (int i = 0; i < E / V; ++i)
+            v[i].get(f + i * V);
+    }
+};
 template <typename T>
 __device__ __forceinline__ T norm_round(float v)
 {
@@ -121,14 +172,18 @@ __device__ __forceinline__ long long norm_row(long long i, int group, long long 
     return o * gs + (long long)((unsigned)i - o * (unsigned)group) * D;
 }
 
+// 1 / (1 + e^-z) on the multi-function unit: e^-z off by 2^-22 + 2^-23 |z|, the reciprocal by 2^-23 (relative);
+// e^-z = inf gives 0
+__device__ __forceinline__ float norm_sigmoid(float z) { return __fdividef(1.f, 1.f + mufu_ex2(-z * kLog2e)); }
+
 // Sums over a team.  Teams up to a warp: butterfly shuffles inside the team
 // (every lane ends with the same bits).  Larger teams: one value per warp
 // through shared memory, added in warp order; two buffers in turn, so that
 // one barrier per sum is enough (a buffer is rewritten two barriers later).
 struct TeamSum {
-    float *red;   // [2][32]
+    float2 *red;   // [2][32]
     int tpr, warp, w0, nw, buf;
-    __device__ __forceinline__ void init(float *smem, int tpr_)
+    __device__ __forceinline__ void init(float2 *smem, int tpr_)
     {
         red = smem;
         tpr = tpr_;
@@ -137,20 +192,41 @@ struct TeamSum {
         w0 = nw > 1 ? warp / nw * nw : 0;
         buf = 0;
     }
-    __device__ __forceinline__ float operator()(float v)
+    // both sums at once
+    __device__ __forceinline__ float2 operator()(float a, float b)
     {
-        for (int o = (tpr < 32 ? tpr : 32) >> 1; o; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int o = (tpr < 32 ? tpr : 32) >> 1; o; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
         if (nw > 1) {   // uniform over the CTA
             if ((threadIdx.x & 31) == 0)
-                red[buf * 32 + warp] = v;
+                red[buf * 32 + warp] = make_float2(a, b);
             __syncthreads();
-            v = 0.f;
-            for (int i = 0; i < nw; ++i)
-                v += red[buf * 32 + w0 + i];
+            a = b = 0.f;
+            for (int i = 0; i < nw; ++i) {
+                const float2 v = red[buf * 32 + w0 + i];
+                a += v.x;
+                b += v.y;
+            }
             buf ^= 1;
         }
-        return v;
+        return make_float2(a, b);
+    }
+    __device__ __forceinline__ float operator()(float a)
+    {
+        for (int o = (tpr < 32 ? tpr : 32) >> 1; o; o >>= 1)
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (nw > 1) {
+            if ((threadIdx.x & 31) == 0)
+                red[buf * 32 + warp].x = a;
+            __syncthreads();
+            a = 0.f;
+            for (int i = 0; i < nw; ++i)
+                a += red[buf * 32 + w0 + i].x;
+            buf ^= 1;
+        }
+        return a;
     }
 };
 
@@ -179,6 +255,58 @@ __device__ __forceinline__ float norm_rows(float (&v)[E], int how, int D, float 
         v[e] *= rs;
     return rs;
 }
+// mean and 1 / sqrt(. + eps) of two rows at once (how none: 0 and 1), each as norm_rows has them
+template <int E, typename GetA, typename GetB, typename In>
+__device__ __forceinline__ void norm_stats2(GetA getA, int howA, GetB getB, int howB, int D, float eps, TeamSum &sum,
+                                            In in, float2 &mean, float2 &rs)
+{
+    const float invD = 1.f / (float)D;
+    mean = make_float2(0.f, 0.f);
+    rs = make_float2(1.f, 1.f);
+    float v[E];
+    if (howA == kNormLayer || howB == kNormLayer) {
+        float a = 0.f, b = 0.f;
+        if (howA == kNormLayer) {
+            getA(v);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                a += v[e];
+        }
+        if (howB == kNormLayer) {
+            getB(v);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                b += v[e];
+        }
+        mean = sum(a, b);
+        mean.x *= invD;
+        mean.y *= invD;
+    }
+    if (howA == kNormNone && howB == kNormNone)
+        return;
+    float a = 0.f, b = 0.f;
+    if (howA != kNormNone) {
+        getA(v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float d = in(e) ? v[e] - mean.x : 0.f;
+            a = fmaf(d, d, a);
+        }
+    }
+    if (howB != kNormNone) {
+        getB(v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float d = in(e) ? v[e] - mean.y : 0.f;
+            b = fmaf(d, d, b);
+        }
+    }
+    const float2 q = sum(a, b);
+    if (howA != kNormNone)
+        rs.x = 1.f / sqrtf(q.x * invD + eps);
+    if (howB != kNormNone)
+        rs.y = 1.f / sqrtf(q.y * invD + eps);
+}
 // d <- rs (d - n mean(d n) - [layer] mean(d))
 template <int E, typename In>
 __device__ __forceinline__ void norm_grad(float (&d)[E], const float (&n)[E], float rs, int how, int D,
@@ -191,18 +319,26 @@ __device__ __forceinline__ void norm_grad(float (&d)[E], const float (&n)[E], fl
         a = fmaf(d[e], n[e], a);
         b += d[e];
     }
-    const float ma = sum(a) * invD;
-    const float mb = how == kNormLayer ? sum(b) * invD : 0.f;
+    float ma, mb = 0.f;
+    if (how == kNormLayer) {
+        const float2 m = sum(a, b);
+        ma = m.x * invD;
+        mb = m.y * invD;
+    } else {
+        ma = sum(a) * invD;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e)
         d[e] = in(e) ? rs * (d[e] - n[e] * ma - mb) : 0.f;
 }
 
-// grid: CTAs of blockDim.x / tpr teams, one row per team and step
+// grid: CTAs of blockDim.x / tpr teams, one row per team and step; the next
+// row's vectors are loaded as soon as this row's are converted.  Measured without
+// that, one row per team at a time: the gated norm of 302592 rows of 64 values 49 us.
 template <typename Tin, typename Tr, int V, int E>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
 {
-    __shared__ float red[64];
+    __shared__ float2 red[64];
     const int lane = threadIdx.x % p.tpr, team = threadIdx.x / p.tpr, teams = blockDim.x / p.tpr;
     const int D = p.D;
     auto col = [&](int i) { return (lane + i * p.tpr) * V; };   // first column of vector i
@@ -210,34 +346,38 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
     TeamSum sum;
     sum.init(red, p.tpr);
     const long long step = (long long)gridDim.x * teams;
-    for (long long base = (long long)blockIdx.x * teams; base < p.rows; base += step) {
-        const long long row = base + team;
-        const bool live = row < p.rows;
-        const long long o = live ? row : 0;
-        const Tin *xr = static_cast<const Tin *>(p.x) + norm_row(o, p.group, p.xs, D);
-        const Tin *zr = static_cast<const Tin *>(p.z) + norm_row(o, p.group, p.zs, D);
-        const Tr *rr = static_cast<const Tr *>(p.r) + o * D;
-        float v[E], z[E], r[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            v[e] = z[e] = r[e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < E / V; ++i) {
-            if (live && col(i) < D) {
-                norm_load<Tin, V>(xr, col(i), v + i * V);
-                if (p.z)
-                    norm_load<Tin, V>(zr, col(i), z + i * V);
-                if (p.r)
-                    norm_load<Tr, V>(rr, col(i), r + i * V);
-            }
-        }
+    NormRow<Tin, V, E> xr, zr;
+    NormRow<Tr, V, E> rr;
+    auto load_x = [&](long long o) {
+        const bool live = o < p.rows;
+        xr.load(static_cast<const Tin *>(p.x) + (live ? norm_row(o, p.group, p.xs, D) : 0), live, D, col);
+    };
+    auto load_z = [&](long long o) {
+        const bool live = o < p.rows;
+        if (p.z)
+            zr.load(static_cast<const Tin *>(p.z) + (live ? norm_row(o, p.group, p.zs, D) : 0), live, D, col);
+    };
+    auto load_r = [&](long long o) {
+        const bool live = o < p.rows;
+        if (p.r)
+            rr.load(static_cast<const Tr *>(p.r) + (live ? o * D : 0), live, D, col);
+    };
+    const long long first = (long long)blockIdx.x * teams;
+    load_x(first + team);
+    load_z(first + team);
+    load_r(first + team);
+    for (long long base = first; base < p.rows; base += step) {
+        const long long o = base + team;
+        const bool live = o < p.rows;
+        float v[E], w[E];
+        xr.get(v);
+        load_x(o + step);
         if (p.post != kNormNone) {
             norm_rows<E>(v, p.post, D, p.eps, sum, in);
 #pragma unroll
             for (int i = 0; i < E / V; ++i) {
                 if (col(i) >= D)
                     continue;
-                float w[V];
                 if (p.w_post) {
                     norm_load<float, V>(p.w_post, col(i), w);
 #pragma unroll
@@ -253,27 +393,34 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
             }
         }
         if (p.z) {
+            zr.get(w);
+            load_z(o + step);
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                v[e] *= z[e] / (1.f + expf(-z[e]));
+                v[e] *= w[e] * norm_sigmoid(w[e]);
         }
+        if (p.s) {
 #pragma unroll
-        for (int i = 0; i < E / V; ++i) {
-            if (col(i) >= D)
-                continue;
-            if (p.s) {
-                float w[V];
+            for (int i = 0; i < E / V; ++i) {
+                if (col(i) >= D)
+                    continue;
                 norm_load<float, V>(p.s, col(i), w);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     v[i * V + j] *= w[j];
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[i * V + j] += r[i * V + j];
-            if (live)
-                norm_store<Tr, V>(static_cast<Tr *>(p.r_out) + o * D, col(i), v + i * V);
         }
+        if (p.r) {
+            rr.get(w);
+            load_r(o + step);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                v[e] += w[e];
+        }
+#pragma unroll
+        for (int i = 0; i < E / V; ++i)
+            if (live && col(i) < D)
+                norm_store<Tr, V>(static_cast<Tr *>(p.r_out) + o * D, col(i), v + i * V);
         if (p.pre != kNormNone) {
             // the norm reads r' before its rounding to r's type
             norm_rows<E>(v, p.pre, D, p.eps, sum, in);
@@ -281,7 +428,6 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
             for (int i = 0; i < E / V; ++i) {
                 if (col(i) >= D)
                     continue;
-                float w[V];
                 if (p.w_pre) {
                     norm_load<float, V>(p.w_pre, col(i), w);
 #pragma unroll
@@ -301,21 +447,27 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
     }
 }
 
-// dynamic shared memory: blockDim.x * E floats (the teams' column sums)
-template <typename Tin, typename Tr, int V, int E>
+// dynamic shared memory: blockDim.x * E floats (the teams' column sums).  BIAS:
+// the sums for biases are kept too (two of five, 16 registers).  The next row's
+// vectors are on their way while a row's sums go round, and both norms' statistics
+// go round together: with loads where they are used and every sum by itself,
+// 12544 rows of 1024 values with every part took 144 us.
+template <typename Tin, typename Tr, int V, int E, bool BIAS>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
 {
+    constexpr int NC = BIAS ? kNormCols : 3;
+    constexpr bool ahead = E == 8;   // rows of 4097 values and more have no registers for it
     extern __shared__ __align__(16) float csum[];
-    __shared__ float red[64];
+    __shared__ float2 red[64];
     const int lane = threadIdx.x % p.tpr, team = threadIdx.x / p.tpr, teams = blockDim.x / p.tpr;
     const int D = p.D;
     auto col = [&](int i) { return (lane + i * p.tpr) * V; };
     auto in = [&](int e) { return (lane + e / V * p.tpr) * V + e % V < D; };
     TeamSum sum;
     sum.init(red, p.tpr);
-    float acc[kNormCols][E];
+    float acc[NC][E];
 #pragma unroll
-    for (int c = 0; c < kNormCols; ++c)
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int e = 0; e < E; ++e)
             acc[c][e] = 0.f;
@@ -329,23 +481,62 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
         }
     };
     const long long step = (long long)gridDim.x * teams;
-    for (long long base = (long long)blockIdx.x * teams; base < p.rows; base += step) {
-        const long long row = base + team;
-        const bool live = row < p.rows;
-        const long long o = live ? row : 0;
+    NormRow<Tin, V, E> xr, zr, yr;
+    NormRow<Tr, V, E> rr, gr;
+    auto row_x = [&](long long o) {
+        const bool live = o < p.rows;
+        xr.load(static_cast<const Tin *>(p.x) + (live ? norm_row(o, p.group, p.xs, D) : 0), live, D, col);
+    };
+    auto row_z = [&](long long o) {
+        const bool live = o < p.rows;
+        if (p.z)
+            zr.load(static_cast<const Tin *>(p.z) + (live ? norm_row(o, p.group, p.zs, D) : 0), live, D, col);
+    };
+    auto row_pre = [&](long long o) {
+        const bool live = o < p.rows;
+        if (p.pre != kNormNone) {
+            rr.load(static_cast<const Tr *>(p.r) + (live ? o * D : 0), live, D, col);
+            yr.load(static_cast<const Tin *>(p.dy) + (live ? o * D : 0), live, D, col);
+        }
+    };
+    auto row_g = [&](long long o) {
+        const bool live = o < p.rows;
+        if (p.dr_out)
+            gr.load(static_cast<const Tr *>(p.dr_out) + (live ? o * D : 0), live, D, col);
+    };
+    const long long first = (long long)blockIdx.x * teams;
+    if constexpr (ahead) {
+        row_pre(first + team);
+        row_g(first + team);
+        row_x(first + team);
+        row_z(first + team);
+    }
+    for (long long base = first; base < p.rows; base += step) {
+        const long long o = base + team;
+        const bool live = o < p.rows;
         float g[E], a[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            g[e] = a[e] = 0.f;
+            g[e] = 0.f;
+        if constexpr (!ahead) {
+            row_pre(o);
+            row_g(o);
+            row_x(o);
+            row_z(o);
+        }
+        // both norms' statistics in one round of sums
+        float2 mean, rs;
+        norm_stats2<E>([&](float (&v)[E]) { rr.get(v); }, p.pre, [&](float (&v)[E]) { xr.get(v); }, p.post, D, p.eps,
+                       sum, in, mean, rs);
         // G: the gradient of r'
         if (p.pre != kNormNone) {
+            rr.get(a);
+            yr.get(g);
+            if constexpr (ahead)
+                row_pre(o + step);
 #pragma unroll
-            for (int i = 0; i < E / V; ++i)
-                if (live && col(i) < D) {
-                    norm_load<Tr, V>(static_cast<const Tr *>(p.r) + o * D, col(i), a + i * V);
-                    norm_load<Tin, V>(static_cast<const Tin *>(p.dy) + o * D, col(i), g + i * V);
-                }
-            const float rs = norm_rows<E>(a, p.pre, D, p.eps, sum, in);
+            for (int e = 0; e < E; ++e)
+                a[e] = in(e) ? (a[e] - mean.x) * rs.x : 0.f;
 #pragma unroll
             for (int i = 0; i < E / V; ++i) {
                 float w[V];
@@ -354,23 +545,21 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const int e = i * V + j;
-                    acc[3][e] = fmaf(g[e], a[e], acc[3][e]);
-                    acc[4][e] += g[e];
+                    acc[2][e] = fmaf(g[e], a[e], acc[2][e]);
+                    if constexpr (BIAS)
+                        acc[4][e] += g[e];
                     g[e] = col(i) < D ? g[e] * w[j] : 0.f;
                 }
             }
-            norm_grad<E>(g, a, rs, p.pre, D, sum, in);
+            norm_grad<E>(g, a, rs.x, p.pre, D, sum, in);
         }
         if (p.dr_out) {
+            gr.get(a);
+            if constexpr (ahead)
+                row_g(o + step);
 #pragma unroll
-            for (int i = 0; i < E / V; ++i)
-                if (live && col(i) < D) {
-                    float w[V];
-                    norm_load<Tr, V>(static_cast<const Tr *>(p.dr_out) + o * D, col(i), w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        g[i * V + j] += w[j];
-                }
+            for (int e = 0; e < E; ++e)
+                g[e] += a[e];
         }
         if (p.dr) {
 #pragma unroll
@@ -379,38 +568,35 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
                     norm_store<Tr, V>(static_cast<Tr *>(p.dr) + o * D, col(i), g + i * V);
         }
         // the branch again: n, p, t
-        const Tin *xr = static_cast<const Tin *>(p.x) + norm_row(o, p.group, p.xs, D);
+        xr.get(a);
+        if constexpr (ahead)
+            row_x(o + step);
+        if (p.post != kNormNone) {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            a[e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < E / V; ++i)
-            if (live && col(i) < D)
-                norm_load<Tin, V>(xr, col(i), a + i * V);
-        float rs = 0.f;
-        if (p.post != kNormNone)
-            rs = norm_rows<E>(a, p.post, D, p.eps, sum, in);
+            for (int e = 0; e < E; ++e)
+                a[e] = in(e) ? (a[e] - mean.y) * rs.y : 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < E / V; ++i) {
-            const bool on = live && col(i) < D;
+            const bool on = col(i) < D;
             float w[V], b[V], s[V], z[V], dz[V];
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 w[j] = b[j] = s[j] = z[j] = 0.f;
-            if (col(i) < D) {
+            if (on) {
                 vec(p.post != kNormNone ? p.w_post : nullptr, i, 1.f, w);
                 vec(p.post != kNormNone ? p.b_post : nullptr, i, 0.f, b);
                 vec(p.s, i, 1.f, s);
             }
-            if (p.z && on)
-                norm_load<Tin, V>(static_cast<const Tin *>(p.z) + norm_row(o, p.group, p.zs, D), col(i), z);
+            if (p.z)
+                zr.v[i].get(z);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int e = i * V + j;
                 const float pv = fmaf(a[e], w[j], b[j]);
                 float gate = 1.f, dgate = 0.f;
                 if (p.z) {
-                    const float sg = 1.f / (1.f + expf(-z[j]));
+                    const float sg = norm_sigmoid(z[j]);
                     gate = z[j] * sg;
                     dgate = sg * fmaf(z[j], 1.f - sg, 1.f);
                 }
@@ -419,14 +605,17 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
                 dz[j] = dt * pv * dgate;
                 const float dp = dt * gate;
                 acc[1][e] = fmaf(dp, a[e], acc[1][e]);
-                acc[2][e] += dp;
+                if constexpr (BIAS)
+                    acc[3][e] += dp;
                 g[e] = dp * w[j];
             }
-            if (p.dz && on)
+            if (p.dz && live && on)
                 norm_store<Tin, V>(static_cast<Tin *>(p.dz) + o * D, col(i), dz);
         }
+        if constexpr (ahead)
+            row_z(o + step);
         if (p.post != kNormNone)
-            norm_grad<E>(g, a, rs, p.post, D, sum, in);
+            norm_grad<E>(g, a, rs.y, p.post, D, sum, in);
 #pragma unroll
         for (int i = 0; i < E / V; ++i)
             if (live && col(i) < D)
@@ -434,7 +623,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
     }
     // the CTA's column sums, its teams in order
 #pragma unroll
-    for (int c = 0; c < kNormCols; ++c) {
+    for (int c = 0; c < NC; ++c) {
         if (!(p.cols >> c & 1))
             continue;
         __syncthreads();
@@ -458,27 +647,29 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
 struct NormSums {
     float *out[kNormCols];
 };
-// out[c][d] = sum over the partials, in order: 8 interleaved runs of CTAs, then the runs.  grid (ceil(D / 32),
-// kNormCols), 256 threads
-static __global__ void __launch_bounds__(256) norm_colsum_kernel(const float *part, NormSums o, int nparts, int D)
+// out[c][d] = sum over the partials, in order: 32 interleaved runs of CTAs, then the runs.  grid (ceil(D / 32),
+// kNormCols), 1024 threads (256 threads and 8 runs took 15 us for 296 partials of 1024 columns)
+static __global__ void __launch_bounds__(1024) norm_colsum_kernel(const float *part, NormSums o, int nparts, int D)
 {
-    __shared__ float sm[8][32];
+    __shared__ float sm[32][33];
     float *out = o.out[blockIdx.y];
     if (!out)
         return;
-    const int d = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, d = blockIdx.x * 32 + lane, run = threadIdx.x >> 5;
     float v = 0.f;
-    if (d < D)
-        for (int i = run; i < nparts; i += 8)
+    if (d < D) {
+#pragma unroll 4
+        for (int i = run; i < nparts; i += 32)
             v += part[((size_t)blockIdx.y * nparts + i) * D + d];
-    sm[run][threadIdx.x & 31] = v;
-    __syncthreads();
-    if (run == 0 && d < D) {
-        v = sm[0][threadIdx.x];
-        for (int i = 1; i < 8; ++i)
-            v += sm[i][threadIdx.x];
-        out[d] = v;
     }
+    sm[run][lane] = v;
+    __syncthreads();
+    // warp `run` sums column `run`
+    v = sm[lane][run];
+    for (int m = 16; m; m >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, m);
+    if (lane == 0 && blockIdx.x * 32 + run < D)
+        out[blockIdx.x * 32 + run] = v;
 }
 
 }  // namespace ss2d
