@@ -112,9 +112,9 @@ int run_chunked(Call &c, bool bwd)
     const size_t n = (size_t)p.nslots, nh = n * p.H, part = ss2d::kTriBytes;
     const size_t kp = pl.npi > 1 ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
     const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
-    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx, vx};
-    size_t off[10], total = 0;
-    for (int i = 0; i < 10; ++i) {
+    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx};
+    size_t off[9], total = 0;
+    for (int i = 0; i < 9; ++i) {
         off[i] = total;
         total += up256(size[i]);
     }
@@ -132,8 +132,7 @@ int run_chunked(Call &c, bool bwd)
     p.Sx = f(5);
     p.dSx = f(6);
     p.Vx = f(7);
-    p.Yx = f(8);
-    p.dXx = f(9);
+    p.dXx = f(8);
     rc = run(c, pl, bwd ? ss2d::kDeltaBwd : ss2d::kDeltaFwd);
     const cudaError_t e = cudaFreeAsync(scratch, c.st);
     if (rc == SS2D_OK && e != cudaSuccess) {

@@ -72,7 +72,7 @@ struct DeltaParams {
     void *dq, *dk, *dv;
     float *dg, *dbeta;
     float *Sx, *dSx;               // S before, dS after each chunk: [DV][DKP] per (slot, head)
-    float *Vx, *Yx, *dXx;          // V', Y, dX: [DV][64] per (slot, head)
+    float *Vx, *dXx;               // V', dX: [DV][64] per (slot, head)
 };
 
 struct DeltaSeq {
@@ -529,57 +529,61 @@ struct PrepLayout {
     static constexpr int bytes = tiles > head ? tiles : head;
 };
 
-// NPI x 64 x DKP bf16 parts of the token rows of q or k into a swizzled tile
-template <typename Tin, int DKP, int NPI>
+// NPI x 64 x DKP bf16 parts of the token rows of q or k into a swizzled tile: by
+// asynchronous copies where the input is its own part (the caller waits for them)
+template <typename Tin, int DKP, int NPI, int NT>
 __device__ __forceinline__ void delta_stage_parts(const DeltaParams &p, const void *base, long long ts, int hk,
-                                                  const DeltaSeq &q, int t0, unsigned char *tile, int nthreads)
+                                                  const DeltaSeq &q, int t0, unsigned char *tile)
 {
     constexpr int RB = DKP * 2, PPR = DKP / 8;
+    static_assert(kDeltaC * PPR % NT == 0, "whole rounds");
     const Tin *src = static_cast<const Tin *>(base) + (long long)hk * p.DK;
-    for (int i = threadIdx.x; i < kDeltaC * PPR; i += nthreads) {
-        const int r = i / PPR, pc = i % PPR;
+#pragma unroll 4
+    for (int k = 0; k < kDeltaC * PPR / NT; ++k) {
+        const int i = k * NT + threadIdx.x, r = i / PPR, pc = i % PPR;
         const bool in = t0 + r < q.len && pc * 8 < p.DK;
-        float v[8];
+        const Tin *row = src + delta_token(p, q, in ? t0 + r : 0) * ts + (in ? pc * 8 : 0);
+        if constexpr (NPI == 1) {
+            cp16(smem_addr(tile) + swz<RB>(r, pc), row, in);
+        } else {
+            float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = 0.f;
-        if (in) {
-            const Tin *row = src + delta_token(p, q, t0 + r) * ts + pc * 8;
-            if constexpr (sizeof(Tin) == 2) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(row);
-                if constexpr (NPI == 1) {
-                    *reinterpret_cast<uint4 *>(tile + swz<RB>(r, pc)) = u;
-                    continue;
-                }
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int j = 0; j < 8; ++j)
+                v[j] = 0.f;
+            if (in) {
+                if constexpr (sizeof(Tin) == 2) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(row);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[2 * j] = half_bits_to_f32<Tin>(w[j] & 0xffffu);
-                    v[2 * j + 1] = half_bits_to_f32<Tin>(w[j] >> 16);
+                    for (int j = 0; j < 4; ++j) {
+                        v[2 * j] = half_bits_to_f32<Tin>(w[j] & 0xffffu);
+                        v[2 * j + 1] = half_bits_to_f32<Tin>(w[j] >> 16);
+                    }
+                } else {
+                    const float4 f0 = *reinterpret_cast<const float4 *>(row);
+                    const float4 f1 = *reinterpret_cast<const float4 *>(row + 4);
+                    v[0] = f0.x;
+                    v[1] = f0.y;
+                    v[2] = f0.z;
+                    v[3] = f0.w;
+                    v[4] = f1.x;
+                    v[5] = f1.y;
+                    v[6] = f1.z;
+                    v[7] = f1.w;
                 }
-            } else {
-                const float4 f0 = *reinterpret_cast<const float4 *>(row);
-                const float4 f1 = *reinterpret_cast<const float4 *>(row + 4);
-                v[0] = f0.x;
-                v[1] = f0.y;
-                v[2] = f0.z;
-                v[3] = f0.w;
-                v[4] = f1.x;
-                v[5] = f1.y;
-                v[6] = f1.z;
-                v[7] = f1.w;
             }
+            uint32_t w[4][NPI];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                split2<NPI>(v[2 * j], v[2 * j + 1], w[j]);
+#pragma unroll
+            for (int n = 0; n < NPI; ++n)
+                *reinterpret_cast<uint4 *>(tile + n * kDeltaC * RB + swz<RB>(r, pc)) =
+                    make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
         }
-        uint32_t w[4][NPI];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            split2<NPI>(v[2 * j], v[2 * j + 1], w[j]);
-#pragma unroll
-        for (int n = 0; n < NPI; ++n)
-            *reinterpret_cast<uint4 *>(tile + n * kDeltaC * RB + swz<RB>(r, pc)) =
-                make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
     }
 }
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
 // acc (16 rows x 8 NT columns of a warp) += rows r0.. of tile A times rows n0.. of tile B, transposed: sums over DKP
 template <int DKP, int NPI, int NT>
@@ -655,10 +659,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hk = blockIdx.y, G = p.H / p.HK, t0 = c * kDeltaC;
     unsigned char *kt = dsm, *qt = dsm + NPI * PB;
-    delta_stage_parts<Tin, DKP, NPI>(p, p.k, p.ks, hk, q, t0, kt, kPrepThreads);
-    delta_stage_parts<Tin, DKP, NPI>(p, p.q, p.qs, hk, q, t0, qt, kPrepThreads);
+    delta_stage_parts<Tin, DKP, NPI, kPrepThreads>(p, p.k, p.ks, hk, q, t0, kt);
+    delta_stage_parts<Tin, DKP, NPI, kPrepThreads>(p, p.q, p.qs, hk, q, t0, qt);
     if (warp == 3)
         delta_decays(p, q, t0, hk * G, ch, cl, be);
+    cp_wait();
     __syncthreads();
     if (NPI > 1) {   // scratch copies, rows in order (not swizzled)
         const long long base = ((long long)blockIdx.x * p.HK + hk) * NPI * PB;

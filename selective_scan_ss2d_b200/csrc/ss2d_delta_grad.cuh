@@ -7,18 +7,19 @@
 //     GP = scale D dP,         GA = beta D dA,     E = dP P + dA A
 //     dq = scale e^c (dO S^T) + GP K
 //     dk = dR S^T + e^{c_last - c} (V' dS^T) + GP^T Q + GA K + GA^T K,   dR = -beta e^c dX
-//     dbeta = dX.Y + sum_j D (k.k) dA
-//     dc = row sums of E - column sums of E + q.(scale e^c dO S^T) + dR.(K S) - kl,
+//     rd = e^c k.(dX S^T),     dbeta = dX.V - rd + sum_j D (k.k) dA
+//     dc = row sums of E - column sums of E + q.(scale e^c dO S^T) - beta rd - kl,
 //          and on the last token sum kl + e^{c_last} S.dS,    kl = k.(e^{c_last - c} V' dS^T)
 //     dg = sums of dc from the chunk's end
-// with e^c (K S) = V - Y.  (dv = beta dX is written by the reverse chain.)  A CTA of
+// (dv = beta dX is written by the reverse chain.)  A CTA of
 // 8 warps has one (slot, key head) and goes through its value heads in order, so that the
 // gradients of shared keys and queries are sums in a fixed order: warp w
 // holds rows 16 (w % 4) .. + 15 and half w / 4 of the columns of dq, dk (over DK)
-// and of dP, dA (over tokens).  DV is gone through in tiles of 32 columns,
-// split into bf16 parts as they are staged.  What reaches a float32 output through
-// dg and dbeta keeps three parts; dk's first term and the products with GP and
-// GA two when they are stored in 16 bits.  Rows of tokens behind the end take no part.
+// and of dP, dA (over tokens).  DV is gone through in tiles of 32 columns:
+// the float32 tiles of S, dS, dX and V' are copied asynchronously while the tile
+// before is multiplied, and split into bf16 parts when they are here.  What reaches a
+// float32 output through dg and dbeta keeps three parts; the products with GP and
+// GA two when dq and dk are stored in 16 bits.  Rows of tokens behind the end take no part.
 //
 // Heads of up to 64 in bfloat16 run two CTAs per SM (128 registers): with one, the kernel
 // stood at 16 % of the tensor pipe, waiting on its staging (808 us for 6144
@@ -46,9 +47,9 @@ struct GradLayout {
     static constexpr int oU = oO + NPI * kDeltaC * ORow;   // V
     static constexpr int oX = oU + NPI * kDeltaC * ORow;
     static constexpr int oV = oX + 3 * XB;
-    static constexpr int oXs = oV + 3 * XB;          // dR
-    static constexpr int oVs = oXs + NPG * XB;       // e^{c_last - c} V'
-    static constexpr int bytes = oVs + 3 * XB;
+    static constexpr int oR = oV + 3 * XB;           // the next tile as it is: S^T, dS^T, dX, V'
+    static constexpr int rS = DVB * DKP * 4, rX = DVB * kDeltaC * 4;
+    static constexpr int bytes = oR + 2 * rS + 2 * rX;
 };
 
 // 8 floats as the parts of a swizzled row piece
@@ -75,18 +76,19 @@ __device__ __forceinline__ void load8(const float *src, float (&v)[8])
     v[6] = b.z;
     v[7] = b.w;
 }
-// 8 input values as the parts of a row piece, parts `part` bytes apart; row null: zeros
+// 8 input values as the parts of a row piece, parts `part` bytes apart, zeros where not `in`; asynchronously where
+// the input is its own part
 template <typename Tin, int NPI>
-__device__ __forceinline__ void put_inputs(unsigned char *dst, int part, const Tin *row)
+__device__ __forceinline__ void put_inputs(unsigned char *dst, int part, const Tin *row, bool in)
 {
     if constexpr (NPI == 1) {
-        *reinterpret_cast<uint4 *>(dst) = row ? *reinterpret_cast<const uint4 *>(row) : make_uint4(0, 0, 0, 0);
+        cp16(smem_addr(dst), row, in);
     } else {
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             v[j] = 0.f;
-        if (row) {
+        if (in) {
             if constexpr (sizeof(Tin) == 4) {
                 load8(row, v);
             } else {
@@ -111,7 +113,7 @@ __device__ __forceinline__ void put_inputs(unsigned char *dst, int part, const T
 
 // SHARED: several value heads share the key head
 template <typename Tin, int DKP, bool SHARED>
-__global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 104 * 1024 ? 2 : 1))
+__global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 107 * 1024 ? 2 : 1))
     delta_grad_kernel(const DeltaParams p)
 {
     using Lay = GradLayout<Tin, DKP>;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
     extern __shared__ __align__(128) unsigned char dsm[];
     __shared__ __align__(16) float vec[3 * kDeltaC];   // e^c, e^{c_last - c}, beta
     __shared__ float ch[kDeltaC], cl[kDeltaC], be[kDeltaC];
-    __shared__ float red[8][kDeltaC], xv[kDeltaC], rsd[8];
+    __shared__ float xv[kDeltaC], rowR[2][kDeltaC], rsd[8];
     __shared__ float rowE[2][kDeltaC], rowB[2][kDeltaC], rowQ[2][kDeltaC], rowK[2][kDeltaC], colE[4][kDeltaC];
     int s, c;
     DeltaSeq q;
@@ -132,17 +134,36 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
     const int nb = (min(q.len - t0, kDeltaC) + 15) / 16;   // blocks of 16 tokens that hold tokens
     const bool act = wr < nb;
     const uint32_t sa = smem_addr(dsm);
-    delta_stage_parts<Tin, DKP, NPI>(p, p.k, p.ks, hk, q, t0, dsm + Lay::oK, kGradThreads);
-    delta_stage_parts<Tin, DKP, NPI>(p, p.q, p.qs, hk, q, t0, dsm + Lay::oQ, kGradThreads);
-    float dqt[SHARED ? NH : 1][4], dk[NH][4];
+    const int tiles = (p.DV + DVB - 1) / DVB;
+    // copies the raw tile n (head by head) of the group: S^T, dS^T, dX, V', rows past DV zero
+    auto raw = [&](int n) {
+        const long long sh = (long long)blockIdx.x * p.H + hk * G + n / tiles;
+        const int d0 = n % tiles * DVB;
+        constexpr int PS = DKP / 4, PX = kDeltaC / 4;   // 16-byte pieces of a row
+#pragma unroll 4
+        for (int i = tid; i < DVB * PS; i += kGradThreads) {
+            const bool on = d0 + i / PS < p.DV;
+            const long long o = (sh * p.DV + d0) * DKP + (on ? i * 4 : 0);
+            cp16(sa + Lay::oR + i * 16, p.Sx + o, on);
+            cp16(sa + Lay::oR + Lay::rS + i * 16, p.dSx + o, on);
+        }
+#pragma unroll 2
+        for (int i = tid; i < DVB * PX; i += kGradThreads) {
+            const bool on = d0 + i / PX < p.DV;
+            const long long o = (sh * p.DV + d0) * kDeltaC + (on ? i * 4 : 0);
+            cp16(sa + Lay::oR + 2 * Lay::rS + i * 16, p.dXx + o, on);
+            cp16(sa + Lay::oR + 2 * Lay::rS + Lay::rX + i * 16, p.Vx + o, on);
+        }
+    };
+    delta_stage_parts<Tin, DKP, NPI, kGradThreads>(p, p.k, p.ks, hk, q, t0, dsm + Lay::oK);
+    delta_stage_parts<Tin, DKP, NPI, kGradThreads>(p, p.q, p.qs, hk, q, t0, dsm + Lay::oQ);
+    raw(0);
+    float dqt[SHARED ? NH : 1][4], dkt[SHARED ? NH : 1][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
-        for (int n = 0; n < NH; ++n) {
-            dk[n][j] = 0.f;
-            if constexpr (SHARED)
-                dqt[n][j] = 0.f;
-        }
+        for (int n = 0; n < (SHARED ? NH : 1); ++n)
+            dqt[n][j] = dkt[n][j] = 0.f;
     }
     const int i0 = wr * 16 + g8;   // the lane's rows: i0, i0 + 8
     // the lane's two values of row i, tile nt of its half, of the staged q or k
@@ -157,7 +178,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
         }
         return v;
     };
-    float dq[NH][4];
+    float dq[NH][4], dk[NH][4];
     for (int hi = 0; hi < G; ++hi) {
         const int h = hk * G + hi;
         const long long sh = (long long)blockIdx.x * p.H + h;
@@ -166,7 +187,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
             delta_decays(p, q, t0, h, ch, cl, be);
         if (tid >= 64)
             vec[tid - 64] = p.vec[sh * 3 * kDeltaC + tid - 64];
-        float dk2[NH][4], dP[4][4], dA[4][4], xd[2][4], bd[8], sd = 0.f;
+        float dk2[NH][4], dP[4][4], dA[4][4], xd[2][4], sd = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -174,68 +195,46 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                 dP[n][j] = dA[n][j] = 0.f;
 #pragma unroll
             for (int n = 0; n < NH; ++n)
-                dq[n][j] = dk2[n][j] = 0.f;
+                dq[n][j] = dk[n][j] = dk2[n][j] = 0.f;
             xd[0][j] = xd[1][j] = 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            bd[j] = 0.f;
         const int tr = tid >> 3, tk = (tid & 7) * 8;   // a thread's piece of a token tile: 8 tokens from tk of row tr
-        for (int d0 = 0; d0 < p.DV; d0 += DVB) {
-            __syncthreads();
-            // S^T, dS^T
+        for (int ti = 0; ti < tiles; ++ti) {
+            const int d0 = ti * DVB;
+            cp_wait();
+            __syncthreads();   // the raw tile is here, the last tile's parts are read
+            for (int i = tid; i < kDeltaC * (DVB / 8); i += kGradThreads) {   // dO and V, rows of DVB columns
+                const int r = i / (DVB / 8), pc = i % (DVB / 8), t = t0 + r, d = d0 + pc * 8;
+                const bool in = t < q.len && d < p.DV;
+                const long long tok = delta_token(p, q, in ? t : 0);
+                const Tin *od = static_cast<const Tin *>(p.dout) + (tok * p.H + h) * p.DV + (in ? d : 0);
+                const Tin *vd = static_cast<const Tin *>(p.v) + tok * p.vs + (long long)h * p.DV + (in ? d : 0);
+                put_inputs<Tin, NPI>(dsm + Lay::oO + r * Lay::ORow + pc * 16, kDeltaC * Lay::ORow, od, in);
+                put_inputs<Tin, NPI>(dsm + Lay::oU + r * Lay::ORow + pc * 16, kDeltaC * Lay::ORow, vd, in);
+            }
+            const float *rs = reinterpret_cast<const float *>(dsm + Lay::oR);
             for (int i = tid; i < DVB * (DKP / 8); i += kGradThreads) {
                 const int r = i / (DKP / 8), pc = i % (DKP / 8);
                 float a[8], b[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    a[j] = b[j] = 0.f;
-                if (d0 + r < p.DV) {
-                    const long long o = (sh * p.DV + d0 + r) * DKP + pc * 8;
-                    load8(p.Sx + o, a);
-                    load8(p.dSx + o, b);
-                }
+                load8(rs + i * 8, a);
+                load8(rs + Lay::rS / 4 + i * 8, b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     sd = fmaf(a[j], b[j], sd);
                 put_parts<3, RBK>(dsm + Lay::oS, Lay::SB, r, pc, a);
                 put_parts<3, RBK>(dsm + Lay::oS + 3 * Lay::SB, Lay::SB, r, pc, b);
             }
-            if (tr < DVB) {   // dX, V' and their scaled forms; dX.Y
-                float x[8], v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = v[j] = 0.f;
-                if (d0 + tr < p.DV) {
-                    const long long o = (sh * p.DV + d0 + tr) * kDeltaC + tk;
-                    float y[8];
-                    load8(p.dXx + o, x);
-                    load8(p.Vx + o, v);
-                    load8(p.Yx + o, y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        bd[j] = fmaf(x[j], y[j], bd[j]);
-                }
+            if (tr < DVB) {
+                float x[8];
+                load8(rs + Lay::rS / 2 + tr * kDeltaC + tk, x);
                 put_parts<3, 128>(dsm + Lay::oX, Lay::XB, tr, tid & 7, x);
-                put_parts<3, 128>(dsm + Lay::oV, Lay::XB, tr, tid & 7, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] *= -vec[2 * kDeltaC + tk + j] * vec[tk + j];
-                    v[j] *= vec[kDeltaC + tk + j];
-                }
-                put_parts<NPG, 128>(dsm + Lay::oXs, Lay::XB, tr, tid & 7, x);
-                put_parts<3, 128>(dsm + Lay::oVs, Lay::XB, tr, tid & 7, v);
+                load8(rs + Lay::rS / 2 + Lay::rX / 4 + tr * kDeltaC + tk, x);
+                put_parts<3, 128>(dsm + Lay::oV, Lay::XB, tr, tid & 7, x);
             }
-            for (int i = tid; i < kDeltaC * (DVB / 8); i += kGradThreads) {   // dO and V, rows of DVB columns
-                const int r = i / (DVB / 8), pc = i % (DVB / 8), t = t0 + r, d = d0 + pc * 8;
-                const bool in = t < q.len && d < p.DV;
-                const long long tok = delta_token(p, q, in ? t : 0);
-                const Tin *od = static_cast<const Tin *>(p.dout) + (tok * p.H + h) * p.DV + d;
-                const Tin *vd = static_cast<const Tin *>(p.v) + tok * p.vs + (long long)h * p.DV + d;
-                put_inputs<Tin, NPI>(dsm + Lay::oO + r * Lay::ORow + pc * 16, kDeltaC * Lay::ORow, in ? od : nullptr);
-                put_inputs<Tin, NPI>(dsm + Lay::oU + r * Lay::ORow + pc * 16, kDeltaC * Lay::ORow, in ? vd : nullptr);
-            }
-            __syncthreads();
+            cp_wait();
+            __syncthreads();   // the parts are here, the raw tile is free
+            if (hi * tiles + ti + 1 < G * tiles)
+                raw(hi * tiles + ti + 1);
             if (act) {
 #pragma unroll
                 for (int ks = 0; ks < DVB / 16; ++ks) {
@@ -264,6 +263,10 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                             if (wc * 2 + nt / 2 <= wr)
                                 mma_cols<128, 3, 3, 3>(dA[nt], dA[nt + 1], ax, sa + Lay::oV, Lay::XB, ks * 16,
                                                        wc * 4 + nt);
+#pragma unroll
+                        for (int nt = 0; nt < NH; nt += 2)
+                            mma_cols<RBK, 3, 3, 3>(dk[nt], dk[nt + 1], ax, sa + Lay::oS, Lay::SB, ks * 16,
+                                                   wc * NH + nt);
                         if (wc == 1) {   // the diagonal of dX V^T
                             uint32_t b[NPI][4];
 #pragma unroll
@@ -276,31 +279,15 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                         }
                     }
                     {
-                        uint32_t as[NPG][4];
-                        frag_t<NPG>(sa + Lay::oXs, Lay::XB, ks * 16, wr * 16, as);
+                        uint32_t av[3][4];
+                        frag_t<3>(sa + Lay::oV, Lay::XB, ks * 16, wr * 16, av);
 #pragma unroll
                         for (int nt = 0; nt < NH; nt += 2)
-                            mma_cols<RBK, NPG, NPG, NPG>(dk[nt], dk[nt + 1], as, sa + Lay::oS, Lay::SB, ks * 16,
-                                                         wc * NH + nt);
-                    }
-                    {
-                        uint32_t as[3][4];
-                        frag_t<3>(sa + Lay::oVs, Lay::XB, ks * 16, wr * 16, as);
-#pragma unroll
-                        for (int nt = 0; nt < NH; nt += 2)
-                            mma_cols<RBK, 3, 3, 3>(dk2[nt], dk2[nt + 1], as, sa + Lay::oS + 3 * Lay::SB, Lay::SB,
+                            mma_cols<RBK, 3, 3, 3>(dk2[nt], dk2[nt + 1], av, sa + Lay::oS + 3 * Lay::SB, Lay::SB,
                                                    ks * 16, wc * NH + nt);
                     }
                 }
             }
-        }
-        // sums of the staged pieces: over a warp's four rows, then the warps
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            for (int m = 8; m < 32; m <<= 1)
-                bd[j] += __shfl_xor_sync(0xffffffffu, bd[j], m);
-            if (lane < 8)
-                red[warp][tk + j] = bd[j];
         }
         for (int m = 1; m < 32; m <<= 1)
             sd += __shfl_xor_sync(0xffffffffu, sd, m);
@@ -310,33 +297,42 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
             xv[i0] = g8 & 1 ? xd[0][1] : xd[0][0];
             xv[i0 + 8] = g8 & 1 ? xd[1][3] : xd[1][2];
         }
-        // dq's first term and its product with q; kl
+        // dq's first term and its product with q; dk's two and theirs with k
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            const float f = p.scale * vec[i0 + hf * 8];
-            float dot = 0.f, kl = 0.f;
+            const int i = i0 + hf * 8;
+            const float e = vec[i], f = p.scale * e, fx = -vec[2 * kDeltaC + i] * e, fv = vec[kDeltaC + i];
+            float dot = 0.f, kl = 0.f, rd = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt) {
-                const float2 qv = pair(Lay::oQ, i0 + hf * 8, nt), kv = pair(Lay::oK, i0 + hf * 8, nt);
+                const float2 qv = pair(Lay::oQ, i, nt), kv = pair(Lay::oK, i, nt);
                 float &a = dq[nt][hf * 2], &b = dq[nt][hf * 2 + 1];
                 a *= f;
                 b *= f;
                 dot = fmaf(a, qv.x, fmaf(b, qv.y, dot));
-                kl = fmaf(dk2[nt][hf * 2], kv.x, fmaf(dk2[nt][hf * 2 + 1], kv.y, kl));
-                dk[nt][hf * 2] += dk2[nt][hf * 2];
-                dk[nt][hf * 2 + 1] += dk2[nt][hf * 2 + 1];
+                const float va = fv * dk2[nt][hf * 2], vb = fv * dk2[nt][hf * 2 + 1];
+                kl = fmaf(va, kv.x, fmaf(vb, kv.y, kl));
+                float &x = dk[nt][hf * 2], &y = dk[nt][hf * 2 + 1];
+                rd = fmaf(x, kv.x, fmaf(y, kv.y, rd));
+                x = fmaf(fx, x, va);
+                y = fmaf(fx, y, vb);
                 if constexpr (SHARED) {
                     dqt[nt][hf * 2] += a;
                     dqt[nt][hf * 2 + 1] += b;
+                    dkt[nt][hf * 2] += x;
+                    dkt[nt][hf * 2 + 1] += y;
                 }
             }
+            rd *= e;
             for (int m = 1; m < 4; m <<= 1) {
                 dot += __shfl_xor_sync(0xffffffffu, dot, m);
                 kl += __shfl_xor_sync(0xffffffffu, kl, m);
+                rd += __shfl_xor_sync(0xffffffffu, rd, m);
             }
             if ((lane & 3) == 0) {
-                rowQ[wc][i0 + hf * 8] = dot;
-                rowK[wc][i0 + hf * 8] = kl;
+                rowQ[wc][i] = dot;
+                rowK[wc][i] = kl;
+                rowR[wc][i] = rd;
             }
         }
         // k.k and q.k of the warp's rows and tokens
@@ -418,15 +414,12 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                float b = 0.f;
-                for (int w = 0; w < 8; ++w)
-                    b += red[w][i];
-                const float kl = rowK[0][i] + rowK[1][i];
+                const float kl = rowK[0][i] + rowK[1][i], rd = rowR[0][i] + rowR[1][i];
                 kls += kl;
                 const float E = (rowE[0][i] + rowE[1][i]) - ((colE[0][i] + colE[1][i]) + (colE[2][i] + colE[3][i]));
-                dc[e] = ((E + (rowQ[0][i] + rowQ[1][i])) - be[i] * (xv[i] - b)) - kl;
+                dc[e] = ((E + (rowQ[0][i] + rowQ[1][i])) - be[i] * rd) - kl;
                 if (t0 + i < q.len)
-                    p.dbeta[delta_token(p, q, t0 + i) * p.H + h] = b + (rowB[0][i] + rowB[1][i]);
+                    p.dbeta[delta_token(p, q, t0 + i) * p.H + h] = (xv[i] - rd) + (rowB[0][i] + rowB[1][i]);
             }
             for (int m = 1; m < 32; m <<= 1)
                 kls += __shfl_xor_sync(0xffffffffu, kls, m);
@@ -451,11 +444,17 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
         }
         // GP K into dq; GP^T Q, GA K, GA^T K into dk
         if (act) {
-            auto &dqs = [&]() -> auto & {
+            auto &dqs = *[&] {
                 if constexpr (SHARED)
-                    return dqt;
+                    return &dqt;
                 else
-                    return dq;
+                    return &dq;
+            }();
+            auto &dks = *[&] {
+                if constexpr (SHARED)
+                    return &dkt;
+                else
+                    return &dk;
             }();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                     for (int nt = 0; nt < NH; nt += 2) {
                         mma_cols<RBK, NPG, NPI, NPG>(dqs[nt], dqs[nt + 1], a, sa + Lay::oK, PBK, ks * 16,
                                                      wc * NH + nt);
-                        mma_cols<RBK, NPG, NPI, NPG>(dk[nt], dk[nt + 1], b, sa + Lay::oK, PBK, ks * 16, wc * NH + nt);
+                        mma_cols<RBK, NPG, NPI, NPG>(dks[nt], dks[nt + 1], b, sa + Lay::oK, PBK, ks * 16, wc * NH + nt);
                     }
                 }
                 if (ks >= wr && ks < nb) {
@@ -475,8 +474,8 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                     frag_block_t<NPG>(smem_addr(ga) + tri_block(ks, wr), b);
 #pragma unroll
                     for (int nt = 0; nt < NH; nt += 2) {
-                        mma_cols<RBK, NPG, NPI, NPG>(dk[nt], dk[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, wc * NH + nt);
-                        mma_cols<RBK, NPG, NPI, NPG>(dk[nt], dk[nt + 1], b, sa + Lay::oK, PBK, ks * 16, wc * NH + nt);
+                        mma_cols<RBK, NPG, NPI, NPG>(dks[nt], dks[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, wc * NH + nt);
+                        mma_cols<RBK, NPG, NPI, NPG>(dks[nt], dks[nt + 1], b, sa + Lay::oK, PBK, ks * 16, wc * NH + nt);
                     }
                 }
             }
@@ -506,11 +505,13 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
             }
         }
     };
-    if constexpr (SHARED)
+    if constexpr (SHARED) {
         store(p.dq, dqt);
-    else
+        store(p.dk, dkt);
+    } else {
         store(p.dq, dq);
-    store(p.dk, dk);
+        store(p.dk, dk);
+    }
 }
 
 }  // namespace ss2d
