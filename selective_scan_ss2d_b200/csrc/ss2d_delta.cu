@@ -18,6 +18,10 @@ using ss2d::kDeltaC;
 // Calls whose sequences are known to be this short go token by token.
 constexpr int kRecurLen = 4;
 
+// Segments of a long chain: CTAs that they should make, and chunks that each has at least
+constexpr int kSegmentCtas = 148;
+constexpr int kSegmentMin = 8;
+
 struct Call {
     DeltaParams p;
     int dtype;
@@ -109,12 +113,23 @@ int run_chunked(Call &c, bool bwd)
     p.nslots = p.cu ? p.T / kDeltaC + p.nseq : (long long)p.nseq * p.NC;
     if (p.nslots > INT_MAX || p.HK > 65535)
         return SS2D_ERR_SHAPE;
+    // Few long chains are cut into segments of SC chunks, about one for each SM that
+    // a CTA of 64 DV columns can have, when at least four to a chain come of it: the
+    // segments run twice and their states are followed one by one.
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H;
+    const long long sc = (p.nslots * ctas + kSegmentCtas - 1) / kSegmentCtas;
+    if (ctas * p.nseq * 4 <= kSegmentCtas && p.nslots >= 4LL * kSegmentMin * p.nseq)
+        p.SC = (int)(sc < kSegmentMin ? kSegmentMin : sc);
+    const size_t segs = !p.SC ? 0 : p.cu ? p.nslots / p.SC + p.nseq
+                                         : (size_t)p.nseq * ((p.NC + p.SC - 1) / p.SC);
     const size_t n = (size_t)p.nslots, nh = n * p.H, part = ss2d::kTriBytes;
     const size_t kp = pl.npi > 1 ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
     const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
-    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx};
-    size_t off[9], total = 0;
-    for (int i = 0; i < 9; ++i) {
+    const size_t ns = segs * p.H * p.DV * pl.dkp * 4;
+    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx, ns, ns, bwd ? ns : 0, bwd ? ns : 0,
+                           segs * p.H * 3 * pl.dkp * pl.dkp * 2};
+    size_t off[14], total = 0;
+    for (int i = 0; i < 14; ++i) {
         off[i] = total;
         total += up256(size[i]);
     }
@@ -133,6 +148,11 @@ int run_chunked(Call &c, bool bwd)
     p.dSx = f(6);
     p.Vx = f(7);
     p.dXx = f(8);
+    p.Ns = f(9);
+    p.Sin = f(10);
+    p.dNs = f(11);
+    p.dSin = f(12);
+    p.Ms = b + off[13];
     rc = run(c, pl, bwd ? ss2d::kDeltaBwd : ss2d::kDeltaFwd);
     const cudaError_t e = cudaFreeAsync(scratch, c.st);
     if (rc == SS2D_OK && e != cudaSuccess) {

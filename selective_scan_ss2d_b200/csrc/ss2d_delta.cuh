@@ -65,6 +65,11 @@ struct DeltaParams {
     void *kp, *qp;                 // bf16 parts of k and q per (slot, key head): [NPI][64][DKP]
     void *Tp, *Pp;                 // bf16 parts of T and P per (slot, head), packed blocks
     float *vec;                    // per (slot, head): e^c, e^{c_last - c}, beta (64 each)
+    // segments of a long chain: SC chunks each (0: none)
+    int SC;
+    float *Ns, *dNs;               // S^T at a segment's end from zero, dS^T at its start: [DV][DKP] per (segment, head)
+    void *Ms;                      // three bf16 parts of its transition: [DKP][DKP] per (segment, head)
+    float *Sin, *dSin;             // S^T a segment starts from, dS^T it ends with
     // backward
     const void *dout;              // gradient of o
     const float *dh_last;
@@ -125,6 +130,50 @@ __device__ __forceinline__ bool delta_slot(const DeltaParams &p, long long slot,
 __device__ __forceinline__ long long delta_token(const DeltaParams &p, const DeltaSeq &q, int t)
 {
     return q.start + (p.reverse ? q.len - 1 - t : t);
+}
+
+// Segments.  A segment's slot is found like a chunk's: ceil(chunks / SC) slots from
+// here never reach the next sequence's.
+__device__ __forceinline__ long long delta_seg0(const DeltaParams &p, int s, const DeltaSeq &q)
+{
+    return p.cu ? delta_slot0(p, s, q) / p.SC + s : (long long)s * ((p.NC + p.SC - 1) / p.SC);
+}
+// the sequence and chunks [c0, c1) of a chain's unit: a segment, or a whole sequence; false: the unit holds none
+__device__ __forceinline__ bool delta_unit(const DeltaParams &p, long long unit, int &s, DeltaSeq &q, int &c0, int &c1)
+{
+    if (!p.SC) {
+        s = (int)unit;
+        q = delta_seq(p, s);
+        c0 = 0;
+        c1 = (q.len + kDeltaC - 1) / kDeltaC;
+        return true;
+    }
+    int seg;
+    if (!p.cu) {
+        const int n = (p.NC + p.SC - 1) / p.SC;
+        s = (int)(unit / n);
+        seg = (int)(unit - (long long)s * n);
+        q = delta_seq(p, s);
+    } else {
+        int lo = 0, hi = p.nseq - 1;
+        while (lo < hi) {
+            const int m = (lo + hi + 1) >> 1;
+            if (delta_seg0(p, m, delta_seq(p, m)) <= unit)
+                lo = m;
+            else
+                hi = m - 1;
+        }
+        s = lo;
+        q = delta_seq(p, s);
+        const long long d = unit - delta_seg0(p, s, q);
+        if (d < 0 || d > q.len / kDeltaC)
+            return false;
+        seg = (int)d;
+    }
+    const int nc = (q.len + kDeltaC - 1) / kDeltaC;
+    c0 = seg * p.SC;
+    c1 = min(c0 + p.SC, nc);
+    return c0 < c1;
 }
 
 // ---- bf16 parts ------------------------------------------------------------

@@ -14,7 +14,15 @@
 //     dV'^T = dO^T P + e^{c_last - c} (dS^T K^T),  dX^T = dV'^T T,  dR = -beta e^c dX,
 //     dS^T <- e^{c_last} dS^T + (scale e^c dO)^T Q + dR^T K
 // It needs nothing of the forward chain, so that a backward pass runs both in
-// one launch.  A last chunk of up to
+// one launch.
+//
+// A long chain of few heads would leave most SMs idle (three heads of 65536 tokens:
+// 1024 chunks one after the other, 4.2 ms).  Its chunks are cut into segments of SC.
+// S -> M S + N over a segment, so a first pass runs every segment at once, from S = 0
+// with its values for N and from S = 1 without values for M, delta_combine_kernel
+// follows S over the segments, and the chain proper then runs every segment from its
+// state.  The reverse chain's transition is M^T: its first pass adds only its own N.
+//  A last chunk of up to
 // 32 tokens is gone through as half a chunk.
 #pragma once
 
@@ -42,9 +50,12 @@ struct ChainLayout {
 };
 
 // NP parts of intermediate values (states, X, V'), NPP of P and of what only the
-// output is made of.  tile, seq0, seqs: the block's DV tile, first sequence and stride
-template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP, int STAGES>
-__device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int seq0, int seqs)
+// output is made of.  tile: the block's tile of DV, or of DK for a segment's transition
+// (ident).  LOCAL: the first pass over a segment, which only leaves its end; every: also
+// of the segment that no other follows
+template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP, int STAGES, bool LOCAL>
+__device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool ident, long long units,
+                                            bool every = false)
 {
     using Lay = ChainLayout<Tin, DKP, NW, MODE, NP, NPP, STAGES>;
     constexpr int NPI = Lay::NPI, NT = NW * 32, RBK = DKP * 2, PBK = kDeltaC * RBK, NK = DKP / 8;
@@ -54,12 +65,17 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int 
     const int g8 = lane >> 2, t2 = (lane & 3) * 2;   // row and first column of a lane in an accumulator tile
     const int h = blockIdx.y, hk = h / (p.H / p.HK);
     const int dvw = (tile * NW + warp) * 16;   // first of the warp's DV columns
-    const bool won = dvw < p.DV;
-    for (int sn = seq0; sn < p.nseq; sn += seqs) {
-        const DeltaSeq q = delta_seq(p, sn);
-        const int nc = (q.len + kDeltaC - 1) / kDeltaC;
-        const long long slot0 = delta_slot0(p, sn, q);
-        auto chunk = [&](int i) { return MODE == kChainRev ? nc - 1 - i : i; };
+    const bool won = dvw < (LOCAL && ident ? p.DK : p.DV);
+    for (long long unit = blockIdx.z; unit < units; unit += gridDim.z) {
+        int sn, c0, c1;
+        DeltaSeq q;
+        if (!delta_unit(p, unit, sn, q, c0, c1))
+            continue;
+        const long long slot0 = delta_slot0(p, sn, q), su = unit * p.H + h;
+        const int nchunks = (q.len + kDeltaC - 1) / kDeltaC, nc = c1 - c0;
+        if (LOCAL && !every && (MODE == kChainRev ? c0 == 0 : c1 == nchunks))
+            continue;
+        auto chunk = [&](int i) { return MODE == kChainRev ? c1 - 1 - i : c0 + i; };
 
         // copies chunk c's operands into stage st
         auto load = [&](int c, int st) {
@@ -93,7 +109,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int 
                     cp16(base + Lay::oP + i * 16, static_cast<const char *>(p.Pp) + sh * NPP * kTriBytes + i * 16,
                          true);
             constexpr int VPC = Lay::DVT * (int)sizeof(Tin) / 16, VPE = 16 / (int)sizeof(Tin);
-            for (int i = tid; i < kDeltaC * VPC; i += NT) {
+            for (int i = tid; i < (LOCAL && ident ? 0 : kDeltaC * VPC); i += NT) {
                 const int r = i / VPC, pc = i % VPC, d = tile * Lay::DVT + pc * VPE;
                 const bool on = t0 + r < q.len && d < p.DV;
                 const long long tok = delta_token(p, q, on ? t0 + r : 0);
@@ -182,14 +198,20 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int 
         float S[NK][4];
         {
             const float *src = MODE == kChainRev ? p.dh_last : p.h0;
+            const float *sin = (MODE == kChainRev ? p.dSin : p.Sin) + (su * p.DV + dvw + g8) * DKP;
 #pragma unroll
             for (int n = 0; n < NK; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
-                    S[n][j] = src && won && dk < p.DK
-                                  ? src[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv]
-                                  : 0.f;
+                    if constexpr (LOCAL)
+                        S[n][j] = ident && dk == dv && dk < p.DK ? 1.f : 0.f;
+                    else if (p.SC)
+                        S[n][j] = won ? sin[(j >> 1) * 8 * DKP + dk] : 0.f;
+                    else
+                        S[n][j] = src && won && dk < p.DK
+                                      ? src[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv]
+                                      : 0.f;
                 }
         }
         if (nc > 0)
@@ -209,155 +231,54 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int 
             // took 5.9 us a chunk instead of 4.1.
             auto step = [&](auto blocks) {
                 constexpr int NB = decltype(blocks)::value;
-                {
-                    if constexpr (MODE != kChainOut) {
-                        float *dst = MODE == kChainRev ? p.dSx : p.Sx;
+                if constexpr (MODE != kChainOut && !LOCAL) {
+                    float *dst = MODE == kChainRev ? p.dSx : p.Sx;
 #pragma unroll
-                        for (int n = 0; n < NK; ++n)
-                            put(dst, sh, DKP, n, S[n]);
-                    }
-                    float R[8][4], O[8][4];
+                    for (int n = 0; n < NK; ++n)
+                        put(dst, sh, DKP, n, S[n]);
+                }
+                float R[8][4], O[8][4];
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
+                for (int n = 0; n < 8; ++n)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            R[n][j] = O[n][j] = 0.f;
-                    // (K S)^T
+                    for (int j = 0; j < 4; ++j)
+                        R[n][j] = O[n][j] = 0.f;
+                // (K S)^T
 #pragma unroll
-                    for (int ks = 0; ks < DKP / 16; ++ks) {
-                        uint32_t a[NP][4];
-                        frag_a<NP>(S[2 * ks], S[2 * ks + 1], a);
+                for (int ks = 0; ks < DKP / 16; ++ks) {
+                    uint32_t a[NP][4];
+                    frag_a<NP>(S[2 * ks], S[2 * ks + 1], a);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (b < NB)
-                                mma_rows<RBK, NP, NPI, NP>(R[2 * b], R[2 * b + 1], a, sa + Lay::oK, PBK, b * 16, ks * 2);
-                    }
-                    if constexpr (MODE != kChainRev) {
+                    for (int b = 0; b < 4; ++b)
+                        if (b < NB)
+                            mma_rows<RBK, NP, NPI, NP>(R[2 * b], R[2 * b + 1], a, sa + Lay::oK, PBK, b * 16, ks * 2);
+                }
+                if constexpr (MODE != kChainRev) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            if (b < NB) {
-                                float v[2][4];
+                    for (int b = 0; b < 4; ++b) {
+                        if (b < NB) {
+                            float v[2][4] = {};
+                            if (!(LOCAL && ident))
                                 values(sb, b, v[0], v[1]);
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        R[2 * b + e][j] = v[e][j] - eg[b * 16 + e * 8 + t2 + (j & 1)] * R[2 * b + e][j];
-                            }
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    R[2 * b + e][j] *= be[b * 16 + e * 8 + t2 + (j & 1)];   // X
+                                    R[2 * b + e][j] = v[e][j] - eg[b * 16 + e * 8 + t2 + (j & 1)] * R[2 * b + e][j];
                         }
-                        // V'^T = X^T T^T
-                        float W[8][4];
 #pragma unroll
-                        for (int n = 0; n < 8; ++n)
+                        for (int e = 0; e < 2; ++e)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                W[n][j] = 0.f;
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            if (ks >= NB)
-                                continue;
-                            uint32_t a[NP][4];
-                            frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
-#pragma unroll
-                            for (int b = ks; b < 4; ++b)
-                                if (b < NB)
-                                    mma_block_rows<NP, NP, NP>(W[2 * b], W[2 * b + 1], a,
-                                                               sa + Lay::oT + tri_block(b, ks));
-                        }
-                        if constexpr (MODE == kChainOut) {
-                            // O^T = scale e^c (Q S)^T + V'^T P^T
-#pragma unroll
-                            for (int ks = 0; ks < DKP / 16; ++ks) {
-                                uint32_t a[NPP][4];
-                                frag_a<NPP>(S[2 * ks], S[2 * ks + 1], a);
-#pragma unroll
-                                for (int b = 0; b < 4; ++b)
-                                    if (b < NB)
-                                        mma_rows<RBK, NPP, NPI, NPP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oQ, PBK, b * 16,
-                                                                     ks * 2);
-                            }
-#pragma unroll
-                            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    O[n][j] *= p.scale * eg[n * 8 + t2 + (j & 1)];
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                if (ks >= NB)
-                                    continue;
-                                uint32_t a[NPP][4];
-                                frag_a<NPP>(W[2 * ks], W[2 * ks + 1], a);
-#pragma unroll
-                                for (int b = ks; b < 4; ++b)
-                                    if (b < NB)
-                                        mma_block_rows<NPP, NPP, NPP>(O[2 * b], O[2 * b + 1], a,
-                                                                      sa + Lay::oP + tri_block(b, ks));
-                            }
-                            emit(O, p.o, t0);
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < 8; ++n)
-                                put(p.Vx, sh, kDeltaC, n, W[n]);
-                        }
-#pragma unroll
-                        for (int n = 0; n < 8; ++n)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                R[n][j] = W[n][j] * el[n * 8 + t2 + (j & 1)];
-                    } else {
-                        // dV'^T = dO^T P + e^{c_last - c} (K dS)^T: row i of P holds its columns j <= i
-#pragma unroll
-                        for (int n = 0; n < 8; ++n)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                R[n][j] *= el[n * 8 + t2 + (j & 1)];
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            if (ks >= NB)
-                                continue;
-                            float v[2][4];
-                            values(sb, ks, v[0], v[1]);
-                            uint32_t a[NPI][4];
-                            frag_a<NPI>(v[0], v[1], a);
-#pragma unroll
-                            for (int b = 0; b <= ks; ++b)
-                                mma_block_cols<NPI, NPP, NPP>(R[2 * b], R[2 * b + 1], a,
-                                                              sa + Lay::oP + tri_block(ks, b));
-                        }
-                        // dX^T = dV'^T T
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            if (ks >= NB)
-                                continue;
-                            uint32_t a[NP][4];
-                            frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
-#pragma unroll
-                            for (int b = 0; b <= ks; ++b)
-                                mma_block_cols<NP, NP, NP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oT + tri_block(ks, b));
-                        }
-#pragma unroll
-                        for (int n = 0; n < 8; ++n) {
-                            put(p.dXx, sh, kDeltaC, n, O[n]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                O[n][j] *= be[n * 8 + t2 + (j & 1)];
-                                R[n][j] = -eg[n * 8 + t2 + (j & 1)] * O[n][j];   // dR
-                            }
-                        }
-                        emit(O, p.dv, t0);
+                                R[2 * b + e][j] *= be[b * 16 + e * 8 + t2 + (j & 1)];   // X
                     }
-                    // S^T <- e^{c_last} S^T + (e^{c_last - c} V')^T K, or dR^T K + (scale e^c dO)^T Q
-                    const float elast = eg[kDeltaC - 1];
+                    // V'^T = X^T T^T
+                    float W[8][4];
 #pragma unroll
-                    for (int n = 0; n < NK; ++n)
+                    for (int n = 0; n < 8; ++n)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            S[n][j] *= elast;
+                            W[n][j] = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         if (ks >= NB)
@@ -365,21 +286,123 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int 
                         uint32_t a[NP][4];
                         frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
 #pragma unroll
-                        for (int nt = 0; nt < NK; nt += 2)
-                            mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oK, PBK, ks * 16, nt);
-                        if constexpr (MODE == kChainRev) {
-                            float v[2][4];
-                            values(sb, ks, v[0], v[1]);
+                        for (int b = ks; b < 4; ++b)
+                            if (b < NB)
+                                mma_block_rows<NP, NP, NP>(W[2 * b], W[2 * b + 1], a,
+                                                           sa + Lay::oT + tri_block(b, ks));
+                    }
+                    if constexpr (MODE == kChainOut) {
+                        // O^T = scale e^c (Q S)^T + V'^T P^T
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
+                        for (int ks = 0; ks < DKP / 16; ++ks) {
+                            uint32_t a[NPP][4];
+                            frag_a<NPP>(S[2 * ks], S[2 * ks + 1], a);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    v[e][j] *= p.scale * eg[ks * 16 + e * 8 + t2 + (j & 1)];
-                            frag_a<NP>(v[0], v[1], a);
-#pragma unroll
-                            for (int nt = 0; nt < NK; nt += 2)
-                                mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, nt);
+                            for (int b = 0; b < 4; ++b)
+                                if (b < NB)
+                                    mma_rows<RBK, NPP, NPI, NPP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oQ, PBK, b * 16,
+                                                                 ks * 2);
                         }
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                O[n][j] *= p.scale * eg[n * 8 + t2 + (j & 1)];
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            if (ks >= NB)
+                                continue;
+                            uint32_t a[NPP][4];
+                            frag_a<NPP>(W[2 * ks], W[2 * ks + 1], a);
+#pragma unroll
+                            for (int b = ks; b < 4; ++b)
+                                if (b < NB)
+                                    mma_block_rows<NPP, NPP, NPP>(O[2 * b], O[2 * b + 1], a,
+                                                                  sa + Lay::oP + tri_block(b, ks));
+                        }
+                        emit(O, p.o, t0);
+                    } else if constexpr (!LOCAL) {
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+                            put(p.Vx, sh, kDeltaC, n, W[n]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            R[n][j] = W[n][j] * el[n * 8 + t2 + (j & 1)];
+                } else {
+                    // dV'^T = dO^T P + e^{c_last - c} (K dS)^T: row i of P holds its columns j <= i
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            R[n][j] *= el[n * 8 + t2 + (j & 1)];
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        if (ks >= NB)
+                            continue;
+                        float v[2][4];
+                        values(sb, ks, v[0], v[1]);
+                        uint32_t a[NPI][4];
+                        frag_a<NPI>(v[0], v[1], a);
+#pragma unroll
+                        for (int b = 0; b <= ks; ++b)
+                            mma_block_cols<NPI, NPP, NPP>(R[2 * b], R[2 * b + 1], a,
+                                                          sa + Lay::oP + tri_block(ks, b));
+                    }
+                    // dX^T = dV'^T T
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        if (ks >= NB)
+                            continue;
+                        uint32_t a[NP][4];
+                        frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
+#pragma unroll
+                        for (int b = 0; b <= ks; ++b)
+                            mma_block_cols<NP, NP, NP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oT + tri_block(ks, b));
+                    }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        if constexpr (!LOCAL)
+                            put(p.dXx, sh, kDeltaC, n, O[n]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            O[n][j] *= be[n * 8 + t2 + (j & 1)];
+                            R[n][j] = -eg[n * 8 + t2 + (j & 1)] * O[n][j];   // dR
+                        }
+                    }
+                    if constexpr (!LOCAL)
+                        emit(O, p.dv, t0);
+                }
+                // S^T <- e^{c_last} S^T + (e^{c_last - c} V')^T K, or dR^T K + (scale e^c dO)^T Q
+                const float elast = eg[kDeltaC - 1];
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        S[n][j] *= elast;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    if (ks >= NB)
+                        continue;
+                    uint32_t a[NP][4];
+                    frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
+#pragma unroll
+                    for (int nt = 0; nt < NK; nt += 2)
+                        mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oK, PBK, ks * 16, nt);
+                    if constexpr (MODE == kChainRev) {
+                        float v[2][4];
+                        values(sb, ks, v[0], v[1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[e][j] *= p.scale * eg[ks * 16 + e * 8 + t2 + (j & 1)];
+                        frag_a<NP>(v[0], v[1], a);
+#pragma unroll
+                        for (int nt = 0; nt < NK; nt += 2)
+                            mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, nt);
                     }
                 }
             };
@@ -394,16 +417,38 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, int 
                 load(chunk(i + 1), 0);
             }
         }
-        float *dst = MODE == kChainRev ? p.dh0 : p.h_last;
-        if (dst && won) {
+        if constexpr (LOCAL) {
+            if (won && ident) {
+                uint32_t *m = static_cast<uint32_t *>(p.Ms);
 #pragma unroll
-            for (int n = 0; n < NK; ++n)
+                for (int n = 0; n < NK; ++n) {
+                    uint32_t w[3], u[3];
+                    split2<3>(S[n][0], S[n][1], w);
+                    split2<3>(S[n][2], S[n][3], u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
-                    if (dk < p.DK)
-                        dst[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] = S[n][j];
+                    for (int k = 0; k < 3; ++k) {
+                        uint32_t *r = m + (((su * 3 + k) * DKP + dvw + g8) * DKP + n * 8 + t2) / 2;
+                        r[0] = w[k];
+                        r[8 * DKP / 2] = u[k];
+                    }
                 }
+            } else if (won) {
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+                    put(MODE == kChainRev ? p.dNs : p.Ns, su, DKP, n, S[n]);
+            }
+        } else {
+            float *dst = MODE == kChainRev ? p.dh0 : p.h_last;
+            if (dst && won && (MODE == kChainRev ? c0 == 0 : c1 == nchunks)) {
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
+                        if (dk < p.DK)
+                            dst[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] = S[n][j];
+                    }
+            }
         }
         __syncthreads();
     }
@@ -417,20 +462,136 @@ template <typename Tin, int DKP, int NW, int NP, int NPP, int STAGES>
 __global__ void
     __launch_bounds__(NW * 32,
                       (chain_ctas<ChainLayout<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>, DKP, STAGES>()))
-        delta_out_kernel(const DeltaParams p)
+        delta_out_kernel(const DeltaParams p, long long units)
 {
-    delta_chain<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>(p, blockIdx.x, blockIdx.z, gridDim.z);
+    delta_chain<Tin, DKP, NW, kChainOut, NP, NPP, STAGES, false>(p, blockIdx.x, false, units);
 }
 // the forward chain and the reverse one, the longer one first
 template <typename Tin, int DKP, int NW, int STAGES>
 __global__ void __launch_bounds__(NW * 32,
                                   (chain_ctas<ChainLayout<Tin, DKP, NW, kChainRev, 3, 3, STAGES>, DKP, STAGES>()))
-    delta_both_kernel(const DeltaParams p)
+    delta_both_kernel(const DeltaParams p, long long units)
 {
     if (blockIdx.x & 1)
-        delta_chain<Tin, DKP, NW, kChainState, 3, 3, STAGES>(p, blockIdx.x >> 1, blockIdx.z, gridDim.z);
+        delta_chain<Tin, DKP, NW, kChainState, 3, 3, STAGES, false>(p, blockIdx.x >> 1, false, units);
     else
-        delta_chain<Tin, DKP, NW, kChainRev, 3, 3, STAGES>(p, blockIdx.x >> 1, blockIdx.z, gridDim.z);
+        delta_chain<Tin, DKP, NW, kChainRev, 3, 3, STAGES, false>(p, blockIdx.x >> 1, false, units);
+}
+
+// first pass over the segments: tiles of DV forward, of DK for the transition, and of DV in reverse (REV)
+template <typename Tin, int DKP, int NP, int STAGES, bool REV>
+__global__ void __launch_bounds__(128, 2) delta_local_kernel(const DeltaParams p, int dvt, int dkt, long long units)
+{
+    const int x = blockIdx.x;
+    if (x < dvt + dkt)
+        delta_chain<Tin, DKP, 4, kChainState, NP, 3, STAGES, true>(p, x < dvt ? x : x - dvt, x >= dvt, units,
+                                                                     REV && x >= dvt);
+    else if constexpr (REV)
+        delta_chain<Tin, DKP, 4, kChainRev, NP, 3, STAGES, true>(p, x - dvt - dkt, false, units);
+}
+
+// The states that the segments of a sequence start from (blockIdx.x even: dS that
+// they end with): S <- M S + N over them, transposed, a warp 16 columns of DV as in
+// the chain.  One step is DKP^2 products of three parts a column; the next
+// transition is copied meanwhile.  Sequences of no tokens pass their state on.
+template <int DKP, bool REV>
+__global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
+{
+    constexpr int RB = DKP * 2, PB = DKP * RB, NK = DKP / 8, STG = 3 * PB;
+    extern __shared__ __align__(128) unsigned char dsm[];
+    const uint32_t sa = smem_addr(dsm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t2 = (lane & 3) * 2;
+    const int h = blockIdx.y, tile = REV ? blockIdx.x >> 1 : blockIdx.x;
+    const bool rev = REV && !(blockIdx.x & 1);
+    const int dvw = (tile * 4 + warp) * 16;
+    const bool won = dvw < p.DV;
+    for (int sn = blockIdx.z; sn < p.nseq; sn += gridDim.z) {
+        const DeltaSeq q = delta_seq(p, sn);
+        const int nc = (q.len + kDeltaC - 1) / kDeltaC, ns = (nc + p.SC - 1) / p.SC;
+        const long long u0 = delta_seg0(p, sn, q);
+        auto seg = [&](int i) { return (u0 + (rev ? ns - 1 - i : i)) * p.H + h; };
+        auto load = [&](int i) {
+            const char *src = static_cast<const char *>(p.Ms) + seg(i) * STG;
+            for (int k = tid; k < STG / 16; k += 128) {
+                const int r = k / (DKP / 8), pc = k % (DKP / 8);   // r counts the parts' rows
+                cp16(sa + (i & 1) * STG + r / DKP * PB + swz<RB>(r % DKP, pc), src + (long long)k * 16, r % DKP < p.DK);
+            }
+        };
+        const float *src = rev ? p.dh_last : p.h0;
+        float S[NK][4];
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
+                S[n][j] =
+                    src && won && dk < p.DK ? src[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] : 0.f;
+            }
+        if (ns > 1)
+            load(0);
+        for (int i = 0; i < ns; ++i) {
+            const long long o = (seg(i) * p.DV + dvw + g8) * DKP + t2;
+            if (won) {
+                float *dst = (rev ? p.dSin : p.Sin) + o;
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(S[n][0], S[n][1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * DKP + n * 8) = make_float2(S[n][2], S[n][3]);
+                }
+            }
+            if (i + 1 == ns)
+                break;
+            cp_wait();
+            __syncthreads();   // the transition is here, the other stage is read
+            if (i + 2 < ns)
+                load(i + 1);
+            if (won) {
+                const uint32_t m = sa + (i & 1) * STG;
+                const float *N = (rev ? p.dNs : p.Ns) + o;
+                float A[NK][4];
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    const float2 a = *reinterpret_cast<const float2 *>(N + n * 8);
+                    const float2 b = *reinterpret_cast<const float2 *>(N + 8 * DKP + n * 8);
+                    A[n][0] = a.x;
+                    A[n][1] = a.y;
+                    A[n][2] = b.x;
+                    A[n][3] = b.y;
+                }
+#pragma unroll
+                for (int ks = 0; ks < DKP / 16; ++ks) {
+                    uint32_t a[3][4];
+                    frag_a<3>(S[2 * ks], S[2 * ks + 1], a);
+                    if (rev) {
+#pragma unroll
+                        for (int nt = 0; nt < NK; nt += 2)
+                            mma_rows<RB, 3, 3, 3>(A[nt], A[nt + 1], a, m, PB, nt * 8, ks * 2);
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NK; nt += 2)
+                            mma_cols<RB, 3, 3, 3>(A[nt], A[nt + 1], a, m, PB, ks * 16, nt);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        S[n][j] = A[n][j];
+            }
+        }
+        float *dst = rev ? p.dh0 : p.h_last;
+        if (ns == 0 && dst && won) {
+#pragma unroll
+            for (int n = 0; n < NK; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
+                    if (dk < p.DK)
+                        dst[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] = S[n][j];
+                }
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace ss2d

@@ -27,6 +27,14 @@ cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
     return cudaGetLastError();
 }
 
+// chains of a pass: segments (every slot that may hold one), or sequences
+inline long long delta_units(const DeltaParams &p)
+{
+    if (!p.SC)
+        return p.nseq;
+    return p.cu ? p.nslots / p.SC + p.nseq : (long long)p.nseq * ((p.NC + p.SC - 1) / p.SC);
+}
+
 template <typename Tin, int DKP, int NW, int NP, int NPP, int STAGES>
 cudaError_t launch_out(const DeltaParams &p, cudaStream_t st)
 {
@@ -35,8 +43,9 @@ cudaError_t launch_out(const DeltaParams &p, cudaStream_t st)
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid((p.DV + NW * 16 - 1) / (NW * 16), p.H, p.nseq < 65535 ? p.nseq : 65535);
-    kern<<<grid, NW * 32, smem, st>>>(p);
+    const long long units = delta_units(p);
+    const dim3 grid((p.DV + NW * 16 - 1) / (NW * 16), p.H, (unsigned)(units < 65535 ? units : 65535));
+    kern<<<grid, NW * 32, smem, st>>>(p, units);
     return cudaGetLastError();
 }
 template <typename Tin, int DKP, int NW, int STAGES>
@@ -47,8 +56,9 @@ cudaError_t launch_both(const DeltaParams &p, cudaStream_t st)
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid(2 * ((p.DV + NW * 16 - 1) / (NW * 16)), p.H, p.nseq < 65535 ? p.nseq : 65535);
-    kern<<<grid, NW * 32, smem, st>>>(p);
+    const long long units = delta_units(p);
+    const dim3 grid(2 * ((p.DV + NW * 16 - 1) / (NW * 16)), p.H, (unsigned)(units < 65535 ? units : 65535));
+    kern<<<grid, NW * 32, smem, st>>>(p, units);
     return cudaGetLastError();
 }
 
@@ -61,7 +71,7 @@ constexpr int chain_stages(int two_bytes) { return two_bytes <= 225 * 1024 ? 2 :
 template <typename Tin, int DKP, int NP, int NPP>
 cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
 {
-    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * p.nseq;
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p);
     constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainOut, NP, NPP, 2>::bytes);
     if (two == 1 || ctas > 2 * 148)
         return launch_out<Tin, DKP, 4, NP, NPP, 1>(p, st);
@@ -70,11 +80,38 @@ cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
 template <typename Tin, int DKP>
 cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
 {
-    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * p.nseq * 2;
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p) * 2;
     constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainRev, 3, 3, 2>::bytes);
     if (two == 1 || ctas > 2 * 148)
         return launch_both<Tin, DKP, 4, 1>(p, st);
     return launch_both<Tin, DKP, 4, two>(p, st);
+}
+
+// the segments' ends and the states that they start from (REV: and end with in reverse)
+template <typename Tin, int DKP, int NP, bool REV>
+cudaError_t launch_segments(const DeltaParams &p, cudaStream_t st)
+{
+    constexpr int MODE = REV ? kChainRev : kChainState;   // the larger layout of the pass
+    constexpr int stages = chain_stages(2 * ChainLayout<Tin, DKP, 4, MODE, NP, 3, 2>::bytes);
+    constexpr int smem = ChainLayout<Tin, DKP, 4, MODE, NP, 3, stages>::bytes;
+    auto kern = delta_local_kernel<Tin, DKP, NP, stages, REV>;
+    cudaError_t e = delta_smem(kern, smem);
+    if (e != cudaSuccess)
+        return e;
+    const int dvt = (p.DV + 63) / 64, dkt = (p.DK + 63) / 64;
+    const long long units = delta_units(p);
+    kern<<<dim3(dvt * (REV ? 2 : 1) + dkt, p.H, (unsigned)(units < 65535 ? units : 65535)), 128, smem, st>>>(p, dvt, dkt,
+                                                                                                          units);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    constexpr int csmem = 2 * 3 * DKP * DKP * 2;
+    auto comb = delta_combine_kernel<DKP, REV>;
+    e = delta_smem(comb, csmem);
+    if (e != cudaSuccess)
+        return e;
+    comb<<<dim3(dvt * (REV ? 2 : 1), p.H, p.nseq < 65535 ? p.nseq : 65535), 128, csmem, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename Tin, int DKP, bool SHARED>
@@ -93,6 +130,8 @@ template <typename Tin, int DKP>
 cudaError_t launch_bwd(const DeltaParams &p, cudaStream_t st)
 {
     cudaError_t e = launch_prep<Tin, DKP, 3, 3>(p, st);
+    if (e == cudaSuccess && p.SC)
+        e = launch_segments<Tin, DKP, 3, true>(p, st);
     if (e == cudaSuccess)
         e = launch_chain_both<Tin, DKP>(p, st);
     if (e != cudaSuccess)
@@ -100,21 +139,21 @@ cudaError_t launch_bwd(const DeltaParams &p, cudaStream_t st)
     return p.H > p.HK ? launch_grad<Tin, DKP, true>(p, st) : launch_grad<Tin, DKP, false>(p, st);
 }
 
+template <typename Tin, int DKP, int NP, int NPP>
+cudaError_t launch_fwd_parts(const DeltaParams &p, cudaStream_t st)
+{
+    cudaError_t e = launch_prep<Tin, DKP, NP, NPP>(p, st);
+    if (e == cudaSuccess && p.SC)
+        e = launch_segments<Tin, DKP, NP, false>(p, st);
+    return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, NP, NPP>(p, st);
+}
 template <typename Tin, int DKP>
 cudaError_t launch_fwd(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st)
 {
-    cudaError_t e;
-    if constexpr (sizeof(Tin) == 4) {
-        e = launch_prep<Tin, DKP, 3, 3>(p, st);
-        return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, 3, 3>(p, st);
-    } else {
-        if (pl.np == 3) {
-            e = launch_prep<Tin, DKP, 3, 2>(p, st);
-            return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, 3, 2>(p, st);
-        }
-        e = launch_prep<Tin, DKP, 2, 2>(p, st);
-        return e != cudaSuccess ? e : launch_chain_out<Tin, DKP, 2, 2>(p, st);
-    }
+    if constexpr (sizeof(Tin) == 4)
+        return launch_fwd_parts<Tin, DKP, 3, 3>(p, st);
+    else
+        return pl.np == 3 ? launch_fwd_parts<Tin, DKP, 3, 2>(p, st) : launch_fwd_parts<Tin, DKP, 2, 2>(p, st);
 }
 
 // Columns of a state per CTA: 128 (or all), fewer while that leaves SMs without work.

@@ -323,6 +323,22 @@ def test_long_chain_and_strong_decay(dtype, decay):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,DK,DV,L", [("bf16", 32, 48, 2100), ("f32", 64, 16, 2048), ("f16", 128, 80, 2050),
+                                           ("bf16", 96, 128, 2600)])
+def test_long_chains_in_segments(dtype, DK, DV, L):
+    """few heads and long sequences: the chain is cut, its segments run from the states that lead to them"""
+    run_bwd(make(1, L, 1, 1, DK, DV, decay=0.3), dtype)
+    run_fwd(make(1, L, 1, 1, DK, DV, decay=0.0), dtype, state=False, reverse=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", [[0, 0, 6500, 6501, 6990], [3, 2900, 2900, 6980, 6990], [0, 64, 640, 6000, 6990]])
+@pytest.mark.parametrize("dtype,reverse", [("bf16", False), ("f32", True)])
+def test_packed_long_chains_in_segments(cu, dtype, reverse):
+    run_bwd(make(1, 7001, 1, 2, 32, 32, decay=0.2), dtype, cu=cu, reverse=reverse)
+
+
+@pytest.mark.gpu
 def test_resets_by_infinite_decay():
     """g = -inf and the lowest float forget the state: the same as a sequence that starts there"""
     a = make(1, 150, 1, 2, 32, 32)
