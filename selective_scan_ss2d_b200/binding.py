@@ -580,8 +580,9 @@ def _delta_sequences(q, cu_seqlens, what):
 
 
 def _like(t, shape, dtype, device, name):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or t.get_device() != device.index or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} device tensor of shape {tuple(shape)}")
 
 
 def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=None,
@@ -608,12 +609,13 @@ def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=No
     if h0 is not None:
         _like(h0, sdims, torch.float32, q.device, "h0")
     if o is None:
-        o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-    _like(o, v.shape, q.dtype, q.device, "o")
-    if h_last is None and final_state:
-        h_last = torch.empty(sdims, dtype=torch.float32, device=q.device)
+        o = _new(v, v.dtype)
+    else:
+        _like(o, v.shape, q.dtype, q.device, "o")
     if h_last is not None:
         _like(h_last, sdims, torch.float32, q.device, "h_last")
+    elif final_state:
+        h_last = torch.empty(sdims, dtype=torch.float32, device=q.device)
     rc = lib().gated_delta_rule_fwd(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(h0), _raw(o),
                                     _raw(h_last), _raw(cu_seqlens), nseq, L, *dims, *strides,
                                     DK ** -0.5 if scale is None else float(scale), int(reverse), dt,
@@ -668,14 +670,15 @@ def gated_delta_rule_step(q, k, v, g, beta, state, slots=None, *, scale=None, o=
     if q.dim() != 3:
         raise ValueError("q must be (B, HK, DK)")
     B, (HK, H, DK, DV) = q.shape[0], dims
-    if state.dim() != 4:
+    if state.dim() != 4 or state.shape[1:] != (H, DK, DV):
         raise ValueError("state must be (states, H, DK, DV)")
-    _like(state, (state.shape[0], H, DK, DV), torch.float32, q.device, "state")
+    _like(state, state.shape, torch.float32, q.device, "state")
     if slots is not None:
         _like(slots, (B,), torch.int32, q.device, "slots")
     if o is None:
-        o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-    _like(o, v.shape, q.dtype, q.device, "o")
+        o = _new(v, v.dtype)
+    else:
+        _like(o, v.shape, q.dtype, q.device, "o")
     rc = lib().gated_delta_rule_step(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(state),
                                      _raw(slots), _raw(o), B, state.shape[0], *dims, *strides,
                                      DK ** -0.5 if scale is None else float(scale), dt,
@@ -699,35 +702,46 @@ def _norm_rows(t, like, name):
     return (t.shape[1] if t.dim() == 3 else 1), t.stride(0)
 
 
-def _norm_prepare(x, z, s, post, w_post, b_post, pre, w_pre, b_pre, rdt, what):
-    if x.dtype not in _DTYPES:
-        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
-    if post not in NORMS or pre not in NORMS:
+def _norm_prepare(x, z, vectors, post, pre, rdt, what):
+    """Checks shared by the block norms; (rows, D, group, strides, codes of post and pre)."""
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {dt}")
+    how = NORMS.get(post), NORMS.get(pre)
+    if None in how:
         raise ValueError("post and pre must be 'none', 'rms' or 'layer'")
     if not x.is_cuda:
         raise ValueError(f"{what} takes device tensors only")
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must have rows of at least one dimension")
-    if rdt not in (torch.float32, x.dtype):
+    if rdt != torch.float32 and rdt != dt:
         raise TypeError("the residual must be float32 or of x's dtype")
-    D = x.shape[-1]
-    if z is not None and (z.dtype != x.dtype or z.shape != x.shape or z.device != x.device):
+    D, dev = shape[-1], x.get_device()
+    if z is not None and (z.dtype != dt or z.shape != shape or not z.is_cuda or z.get_device() != dev):
         raise ValueError("z must have x's dtype, shape and device")
-    for n, t in (("s", s), ("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (D,) or
-                              t.device != x.device or not t.is_contiguous()):
+    for n, t in vectors:
+        if t is not None and (t.dtype != torch.float32 or t.shape != (D,) or not t.is_cuda or
+                              t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{n} must be a contiguous float32 tensor of shape {(D,)} on x's device")
     lx = _norm_rows(x, x, "x")
     lz = _norm_rows(z, x, "z") if z is not None else None
     group = (lx or lz or (1, D))[0]
     xs, zs = (lx or (0, group * D))[1], (lz or (0, group * D))[1]
-    rows = x.numel() // D if D else 0
-    return rows, D, group, xs, zs
+    return (x.numel() // D if D else 0), D, group, xs, zs, how
 
 
 def _rows_like(t, x, dtype, name):
-    if t.dtype != dtype or t.shape != x.shape or t.device != x.device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != x.shape or not t.is_cuda or t.get_device() != x.get_device() or \
+            not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of x's shape and device")
+
+
+def _new(like, dtype):
+    """A contiguous tensor of a shape and device."""
+    if like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
 
 
 def block_norm_fwd(x, *, z=None, r=None, s=None, post="none", w_post=None, b_post=None,
@@ -744,23 +758,25 @@ def block_norm_fwd(x, *, z=None, r=None, s=None, post="none", w_post=None, b_pos
     dtype; s and the weights (D,) float32; each but x may be None.  Returns
     (r', y), y None without a pre norm.  r_out may be r.  Device tensors only."""
     rdt = r.dtype if r is not None else (r_out.dtype if r_out is not None else x.dtype)
-    rows, D, group, xs, zs = _norm_prepare(x, z, s, post, w_post, b_post, pre, w_pre, b_pre, rdt,
-                                           "block_norm_fwd")
+    rows, D, group, xs, zs, how = _norm_prepare(
+        x, z, (("s", s), ("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)),
+        post, pre, rdt, "block_norm_fwd")
     if r is not None:
         _rows_like(r, x, rdt, "r")
     if r_out is None:
-        r_out = torch.empty(x.shape, dtype=rdt, device=x.device)
-    _rows_like(r_out, x, rdt, "r_out")
+        r_out = _new(x, rdt)
+    else:
+        _rows_like(r_out, x, rdt, "r_out")
     if pre == "none":
         y = None
+    elif y is None:
+        y = _new(x, x.dtype)
     else:
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         _rows_like(y, x, x.dtype, "y")
     rc = lib().block_norm_fwd(_raw(x), _raw(z), _raw(r), _raw(s), _raw(w_post), _raw(b_post),
                               _raw(w_pre), _raw(b_pre), _raw(r_out), _raw(y), rows, D, group, xs,
-                              zs, NORMS[post], NORMS[pre], float(eps), _DTYPES[x.dtype],
-                              _DTYPES[rdt], _raw_stream(x.device, stream))
+                              zs, *how, eps, _DTYPES[x.dtype], _DTYPES[rdt],
+                              _raw_stream(x.device, stream))
     _check(rc)
     return r_out, y
 
@@ -779,8 +795,9 @@ def block_norm_bwd(x, dr_out, dy=None, *, r_out=None, z=None, s=None, post="none
     None), ds and the weights' gradients float32; None for what the call does
     not have.  Device tensors only."""
     rdt = dr_out.dtype if dr_out is not None else (r_out.dtype if r_out is not None else x.dtype)
-    rows, D, group, xs, zs = _norm_prepare(x, z, s, post, w_post, b_post, pre, w_pre, b_pre, rdt,
-                                           "block_norm_bwd")
+    rows, D, group, xs, zs, how = _norm_prepare(
+        x, z, (("s", s), ("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)),
+        post, pre, rdt, "block_norm_bwd")
     has_pre = pre != "none"
     if has_pre:
         if r_out is None or dy is None:
@@ -791,20 +808,15 @@ def block_norm_bwd(x, dr_out, dy=None, *, r_out=None, z=None, s=None, post="none
         raise ValueError("block_norm_bwd without a pre norm needs dr_out")
     if dr_out is not None:
         _rows_like(dr_out, x, rdt, "dr_out")
-    new = lambda want, dt: torch.empty(x.shape, dtype=dt, device=x.device) if want else None  # noqa: E731
-    vec = lambda t: torch.empty((D,), dtype=torch.float32, device=x.device) if t is not None else None  # noqa: E731
-    has_post = post != "none"
-    g = dict(dx=new(True, x.dtype), dz=new(z is not None, x.dtype), dr=new(residual, rdt), ds=vec(s),
-             dw_post=vec(w_post) if has_post else None, db_post=vec(b_post) if has_post else None,
-             dw_pre=vec(w_pre) if has_pre else None, db_pre=vec(b_pre) if has_pre else None)
-    rc = lib().block_norm_bwd(_raw(x), _raw(z), _raw(r_out) if has_pre else _raw(None), _raw(s),
+    post_w, pre_w = (w_post, b_post) if post != "none" else (None, None), (w_pre, b_pre) if has_pre else (None, None)
+    vec = [None if t is None else torch.empty_like(t) for t in (s, *post_w, *pre_w)]
+    g = (_new(x, x.dtype), None if z is None else _new(x, x.dtype), _new(x, rdt) if residual else None, *vec)
+    rc = lib().block_norm_bwd(_raw(x), _raw(z), _raw(r_out) if has_pre else None, _raw(s),
                               _raw(w_post), _raw(b_post), _raw(w_pre), _raw(dr_out),
-                              _raw(dy) if has_pre else _raw(None),
-                              *[_raw(g[n]) for n in NORM_GRAD_NAMES], rows, D, group, xs, zs,
-                              NORMS[post], NORMS[pre], float(eps), _DTYPES[x.dtype], _DTYPES[rdt],
-                              _raw_stream(x.device, stream))
+                              _raw(dy) if has_pre else None, *map(_raw, g), rows, D, group, xs, zs,
+                              *how, eps, _DTYPES[x.dtype], _DTYPES[rdt], _raw_stream(x.device, stream))
     _check(rc)
-    return g
+    return dict(zip(NORM_GRAD_NAMES, g))
 
 
 def ss2d_check_waits() -> int:

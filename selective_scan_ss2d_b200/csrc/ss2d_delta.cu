@@ -84,13 +84,16 @@ int run(Call &c, const DeltaPlan &pl, int what)
     cudaError_t e;
     switch (c.dtype) {
     case SS2D_BF16:
-        e = ss2d::launch_delta_bf16(c.p, pl, what, c.st);
+        e = what == ss2d::kDeltaBwd ? ss2d::launch_delta_bwd_bf16(c.p, pl, c.st)
+                                    : ss2d::launch_delta_bf16(c.p, pl, what, c.st);
         break;
     case SS2D_F16:
-        e = ss2d::launch_delta_f16(c.p, pl, what, c.st);
+        e = what == ss2d::kDeltaBwd ? ss2d::launch_delta_bwd_f16(c.p, pl, c.st)
+                                    : ss2d::launch_delta_f16(c.p, pl, what, c.st);
         break;
     default:
-        e = ss2d::launch_delta_f32(c.p, pl, what, c.st);
+        e = what == ss2d::kDeltaBwd ? ss2d::launch_delta_bwd_f32(c.p, pl, c.st)
+                                    : ss2d::launch_delta_f32(c.p, pl, what, c.st);
         break;
     }
     if (e != cudaSuccess) {

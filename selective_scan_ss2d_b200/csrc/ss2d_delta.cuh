@@ -292,13 +292,14 @@ __device__ __forceinline__ void frag_a(const float (&c0)[4], const float (&c1)[4
 // (each accumulation loses up to 2^-23 of the sum, always downwards), so
 // three-part products are summed from zero, smallest parts first, and added to
 // the result by a rounding float32 addition: measured on the float32 backward
-// (32 x 64 heads, 1500 tokens) the gradients are 2.8e-7 off instead of 3.8e-6.  The
-// additions issue in the tensor pipe's shadow.
+// (32 x 64 heads, 1500 tokens) the gradients are 2.8e-7 off instead of 3.8e-6.  The additions
+// issue in the tensor pipe's shadow.  A product of two exact operands
+// is one accumulation for 16 columns, and goes into the result as it is.
 template <int NA, int NB, int KEEP>
 __device__ __forceinline__ void mma_parts(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
                                           const uint32_t (&b)[NB][4])
 {
-    if constexpr (KEEP == 3) {
+    if constexpr (KEEP == 3 && NA * NB > 1) {
         float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int sum = KEEP - 1; sum >= 0; --sum)
@@ -410,10 +411,10 @@ __device__ __forceinline__ void frag_t(uint32_t tile, int part, int k0, int m0, 
 // o = scale (a q.S + (q.k) d).  Bound by reading and writing the states
 // once: DK * DVT * 8 bytes per CTA, in 16-byte pieces along DV.
 constexpr int kRecurThreads = 256;
-constexpr int kRecurRows = 16;   // rows of the state per thread
 
-template <typename Tin>
-__global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaParams p, int DVT)
+// ROWS: rows of the state per thread
+template <typename Tin, int ROWS>
+__global__ void __launch_bounds__(kRecurThreads, ROWS <= 8 ? 4 : 2) delta_recur_kernel(const DeltaParams p, int DVT)
 {
     __shared__ float sk[kDeltaMaxDK], sq[kDeltaMaxDK];
     __shared__ __align__(16) float red[2][kRecurThreads][4];
@@ -437,9 +438,9 @@ __global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaP
             live = !__syncthreads_or(dup) && live;
         }
         const long long srow = (si * p.H + h) * p.DK;
-        float4 S[kRecurRows];
+        float4 S[ROWS];
 #pragma unroll
-        for (int i = 0; i < kRecurRows; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             const int r = rg + i * RG;
             S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             const float *src = p.pool ? p.pool : p.h0;
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaP
             __syncthreads();
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll
-            for (int i = 0; i < kRecurRows; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const int r = rg + i * RG;
                 if (r < p.DK) {
                     const float kv = sk[r], qv = sq[r];
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaP
                 d.z = be * (to_f32(vr[2]) - al * a.z);
                 d.w = be * (to_f32(vr[3]) - al * a.w);
 #pragma unroll
-                for (int i = 0; i < kRecurRows; ++i) {
+                for (int i = 0; i < ROWS; ++i) {
                     const int r = rg + i * RG;
                     if (r < p.DK) {
                         const float kv = sk[r];
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaP
         float *dst = p.pool ? p.pool : p.h_last;
         if (on && live && dst) {
 #pragma unroll
-            for (int i = 0; i < kRecurRows; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const int r = rg + i * RG;
                 if (r < p.DK)
                     *reinterpret_cast<float4 *>(dst + (srow + r) * p.DV + dv0) = S[i];
@@ -558,8 +559,8 @@ __global__ void __launch_bounds__(kRecurThreads) delta_recur_kernel(const DeltaP
 // e^{c_last - c}, beta.  Steps past the sequence's end have k = q = 0, g = 0,
 // beta = 0: they leave the state as it is.
 //
-// 4 warps, warp w the chunk's rows 16 w .. 16 w + 15 of the products.  T = (I + A)^{-1}
-// in 16 x 16 blocks: warp w inverts block (w, w) by forward substitution in
+// 4 warps share the ten 16 x 16 blocks of the products.  T = (I + A)^{-1} by such
+// blocks: warp w inverts block (w, w) by forward substitution in
 // float32 (lane j its column j), then has the blocks below it,
 //     T_iw = -T_ii sum_{w <= m < i} A_im T_mw,   i = w + 1 .. 3,
 // as tensor-core products of bf16 parts, transposed like the chain's, so that
@@ -658,7 +659,11 @@ __device__ __forceinline__ void delta_rows_product(uint32_t A, uint32_t B, int r
     }
 }
 
-// c (as a float and what it lacks) and beta of one head's chunk, by one warp: lane l holds tokens 2l, 2l + 1
+// e^x of a sum of g kept as c log2(e): a float and what it lacks, so that differences of
+// near tokens behind a large sum are exact to float32
+__device__ __forceinline__ float delta_decay(float h, float l) { return mufu_ex2(h + l); }
+
+// c log2(e) (as a float and what it lacks) and beta of one head's chunk, by one warp: lane l holds tokens 2l, 2l + 1
 __device__ __forceinline__ void delta_decays(const DeltaParams &p, const DeltaSeq &q, int t0, int h, float *ch,
                                              float *cl, float *be)
 {
@@ -676,7 +681,7 @@ __device__ __forceinline__ void delta_decays(const DeltaParams &p, const DeltaSe
             gv = gv < kDeltaGFloor ? kDeltaGFloor : gv;   // a NaN stays one
             b[j] = p.beta[i];
         }
-        v[j] = (double)gv;
+        v[j] = (double)gv * 1.4426950408889634;
     }
     double s = v[0] + v[1];
     for (int o = 1; o < 32; o <<= 1) {
@@ -725,14 +730,23 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
                 *reinterpret_cast<const uint4 *>(qt + so);
         }
     }
-    float kk[8][4], qk[8][4];
+    // the ten blocks of the lower triangle, two or three to a warp: 00 30 31, 10 11 32, 20 21, 22 33
+    constexpr int MB = 3;
+    const int nblk = warp < 2 ? 3 : 2;
+    const uint32_t blocks = warp == 0 ? 0x313000u : warp == 1 ? 0x321110u : warp == 2 ? 0x2120u : 0x3322u;
+    auto bi = [&](int n) { return (int)(blocks >> (8 * n + 4) & 15u); };
+    auto bj = [&](int n) { return (int)(blocks >> (8 * n) & 15u); };
+    float kk[MB][2][4], qk[MB][2][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < MB; ++n) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            kk[n][j] = qk[n][j] = 0.f;
-    delta_rows_product<DKP, NPI, 8>(smem_addr(kt), smem_addr(kt), warp * 16, 0, kk);
-    delta_rows_product<DKP, NPI, 8>(smem_addr(qt), smem_addr(kt), warp * 16, 0, qk);
+            kk[n][0][j] = kk[n][1][j] = qk[n][0][j] = qk[n][1][j] = 0.f;
+        if (n < nblk) {
+            delta_rows_product<DKP, NPI, 2>(smem_addr(kt), smem_addr(kt), bi(n) * 16, bj(n) * 16, kk[n]);
+            delta_rows_product<DKP, NPI, 2>(smem_addr(qt), smem_addr(kt), bi(n) * 16, bj(n) * 16, qk[n]);
+        }
+    }
     const uint32_t sA = smem_addr(dsm), sX = sA + Lay::oX;
     float *dg = reinterpret_cast<float *>(dsm + Lay::oD);   // [4][16][20]
     const int nb = (min(q.len - t0, kDeltaC) + 15) / 16;    // 16-token blocks that hold tokens
@@ -747,40 +761,49 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
         __syncthreads();   // the tiles (or the last head's T) are read, the decays are here
         if (tid < kDeltaC) {
             float *vec = p.vec + sh * 3 * kDeltaC;
-            vec[tid] = expf(ch[tid] + cl[tid]);
-            vec[kDeltaC + tid] = expf((ch[kDeltaC - 1] - ch[tid]) + (cl[kDeltaC - 1] - cl[tid]));
+            vec[tid] = delta_decay(ch[tid], cl[tid]);
+            vec[kDeltaC + tid] = delta_decay(ch[kDeltaC - 1] - ch[tid], cl[kDeltaC - 1] - cl[tid]);
             vec[2 * kDeltaC + tid] = be[tid];
         }
-        const int ir = lane >> 2;   // row of the warp's block
+        const int ir = lane >> 2, jr = (lane & 3) * 2;   // row and first column of a lane in an 8 x 8 tile
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            if (n / 2 > warp)
-                continue;   // above the diagonal blocks
-            const int jc = (n & 1) * 8 + (lane & 3) * 2;
+        for (int n = 0; n < MB; ++n) {
+            if (n >= nblk)
+                continue;
+            const int I = bi(n), J = bj(n);
+            const bool diag = I == J;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const int i = warp * 16 + ir + hf * 8;
-                float pv[2], av[2];
+                const int i = ir + hf * 8;
+                const float hi_ = ch[I * 16 + i], lo_ = cl[I * 16 + i], bi_ = be[I * 16 + i];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = n / 2 * 16 + jc + e;
-                    const float D = j <= i ? expf((ch[i] - ch[j]) + (cl[i] - cl[j])) : 0.f;
-                    pv[e] = j <= i ? p.scale * D * qk[n][hf * 2 + e] : 0.f;
-                    av[e] = j < i ? be[i] * D * kk[n][hf * 2 + e] : 0.f;
-                }
-                const uint32_t o = tri_block(warp, n / 2) + tri_piece(ir + hf * 8, n & 1) + (lane & 3) * 4;
-                uint32_t w[NPP], u[NPT];
-                split2<NPP>(pv[0], pv[1], w);
+                for (int t = 0; t < 2; ++t) {
+                    const int j = t * 8 + jr;
+                    const float2 hj = *reinterpret_cast<const float2 *>(ch + J * 16 + j);
+                    const float2 lj = *reinterpret_cast<const float2 *>(cl + J * 16 + j);
+                    float D0 = delta_decay(hi_ - hj.x, lo_ - lj.x), D1 = delta_decay(hi_ - hj.y, lo_ - lj.y);
+                    if (diag) {   // above the diagonal the exponent is positive: dropped, not multiplied by zero
+                        D0 = j <= i ? D0 : 0.f;
+                        D1 = j < i ? D1 : 0.f;
+                    }
+                    const float k0 = kk[n][t][hf * 2], k1 = kk[n][t][hf * 2 + 1];
+                    const float q0 = qk[n][t][hf * 2], q1 = qk[n][t][hf * 2 + 1];
+                    const bool on0 = !diag || j <= i, on1 = !diag || j < i;
+                    const uint32_t o = tri_block(I, J) + tri_piece(i, t) + (lane & 3) * 4;
+                    uint32_t w[NPP], u[NPT];
+                    split2<NPP>(on0 ? p.scale * D0 * q0 : 0.f, on1 ? p.scale * D1 * q1 : 0.f, w);
 #pragma unroll
-                for (int m = 0; m < NPP; ++m)
-                    *reinterpret_cast<uint32_t *>(dsm + Lay::oX + m * kTriBytes + o) = w[m];
-                if (n / 2 < warp) {
-                    split2<NPT>(av[0], av[1], u);
+                    for (int m = 0; m < NPP; ++m)
+                        *reinterpret_cast<uint32_t *>(dsm + Lay::oX + m * kTriBytes + o) = w[m];
+                    if (!diag) {
+                        split2<NPT>(bi_ * D0 * k0, bi_ * D1 * k1, u);
 #pragma unroll
-                    for (int m = 0; m < NPT; ++m)
-                        *reinterpret_cast<uint32_t *>(dsm + m * kTriBytes + o) = u[m];
-                } else {
-                    *reinterpret_cast<float2 *>(dg + (i * 20 + jc)) = make_float2(av[0], av[1]);
+                        for (int m = 0; m < NPT; ++m)
+                            *reinterpret_cast<uint32_t *>(dsm + m * kTriBytes + o) = u[m];
+                    } else {
+                        *reinterpret_cast<float2 *>(dg + ((I * 16 + i) * 20 + j)) =
+                            make_float2(j < i ? bi_ * D0 * k0 : 0.f, j + 1 < i ? bi_ * D1 * k1 : 0.f);
+                    }
                 }
             }
         }

@@ -1,4 +1,4 @@
-// ss2d_delta_bf16.cu -- the gated delta rule's kernels for __nv_bfloat16 inputs.
+// ss2d_delta_bf16.cu -- the gated delta rule's forward kernels for __nv_bfloat16 inputs.
 #include "ss2d_delta_launch.cuh"
 
 namespace ss2d {

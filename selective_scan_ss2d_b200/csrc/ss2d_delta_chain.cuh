@@ -454,17 +454,26 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
     }
 }
 
-// CTAs per SM that the registers are held to: three of four warps where three stages of shared memory fit
-template <typename Lay, int DKP, int STAGES>
-constexpr int chain_ctas() { return STAGES == 1 && DKP == 64 && Lay::bytes <= 74 * 1024 ? 3 : 2; }
+// CTAs per SM that the registers are held to: three of four warps where three stages of shared memory fit and
+// 168 registers do (not the output's chain with three parts: 328 bytes of spills)
+template <typename Lay, int DKP, int STAGES, bool OUT3 = false>
+constexpr int chain_ctas() { return STAGES == 1 && DKP == 64 && Lay::bytes <= 74 * 1024 && !OUT3 ? 3 : 2; }
 
 template <typename Tin, int DKP, int NW, int NP, int NPP, int STAGES>
 __global__ void
     __launch_bounds__(NW * 32,
-                      (chain_ctas<ChainLayout<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>, DKP, STAGES>()))
+                      (chain_ctas<ChainLayout<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>, DKP, STAGES, NP == 3>()))
         delta_out_kernel(const DeltaParams p, long long units)
 {
     delta_chain<Tin, DKP, NW, kChainOut, NP, NPP, STAGES, false>(p, blockIdx.x, false, units);
+}
+// one chain of the backward pass
+template <typename Tin, int DKP, int NW, int STAGES, int MODE>
+__global__ void
+    __launch_bounds__(NW * 32, (chain_ctas<ChainLayout<Tin, DKP, NW, MODE, 3, 3, STAGES>, DKP, STAGES>()))
+        delta_one_kernel(const DeltaParams p, long long units)
+{
+    delta_chain<Tin, DKP, NW, MODE, 3, 3, STAGES, false>(p, blockIdx.x, false, units);
 }
 // the forward chain and the reverse one, the longer one first
 template <typename Tin, int DKP, int NW, int STAGES>
@@ -490,6 +499,7 @@ __global__ void __launch_bounds__(128, 2) delta_local_kernel(const DeltaParams p
         delta_chain<Tin, DKP, 4, kChainRev, NP, 3, STAGES, true>(p, x - dvt - dkt, false, units);
 }
 
+__host__ __device__ constexpr int combine_stages(int dkp) { return dkp == 64 ? 4 : 2; }
 // The states that the segments of a sequence start from (blockIdx.x even: dS that
 // they end with): S <- M S + N over them, transposed, a warp 16 columns of DV as in
 // the chain.  One step is DKP^2 products of three parts a column; the next
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(128, 2) delta_local_kernel(const DeltaParams p
 template <int DKP, bool REV>
 __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
 {
-    constexpr int RB = DKP * 2, PB = DKP * RB, NK = DKP / 8, STG = 3 * PB;
+    constexpr int RB = DKP * 2, PB = DKP * RB, NK = DKP / 8, STG = 3 * PB, STAGES = combine_stages(DKP);
     extern __shared__ __align__(128) unsigned char dsm[];
     const uint32_t sa = smem_addr(dsm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t2 = (lane & 3) * 2;
@@ -514,7 +524,8 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
             const char *src = static_cast<const char *>(p.Ms) + seg(i) * STG;
             for (int k = tid; k < STG / 16; k += 128) {
                 const int r = k / (DKP / 8), pc = k % (DKP / 8);   // r counts the parts' rows
-                cp16(sa + (i & 1) * STG + r / DKP * PB + swz<RB>(r % DKP, pc), src + (long long)k * 16, r % DKP < p.DK);
+                cp16(sa + i % STAGES * STG + r / DKP * PB + swz<RB>(r % DKP, pc), src + (long long)k * 16,
+                     r % DKP < p.DK);
             }
         };
         const float *src = rev ? p.dh_last : p.h0;
@@ -527,8 +538,12 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
                 S[n][j] =
                     src && won && dk < p.DK ? src[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] : 0.f;
             }
-        if (ns > 1)
-            load(0);
+        // one group of copies for each step, empty past the end
+        for (int i = 0; i < STAGES - 1; ++i) {
+            if (i + 1 < ns)
+                load(i);
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+        }
         for (int i = 0; i < ns; ++i) {
             const long long o = (seg(i) * p.DV + dvw + g8) * DKP + t2;
             if (won) {
@@ -541,14 +556,9 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
             }
             if (i + 1 == ns)
                 break;
-            cp_wait();
-            __syncthreads();   // the transition is here, the other stage is read
-            if (i + 2 < ns)
-                load(i + 1);
+            float A[NK][4];
             if (won) {
-                const uint32_t m = sa + (i & 1) * STG;
                 const float *N = (rev ? p.dNs : p.Ns) + o;
-                float A[NK][4];
 #pragma unroll
                 for (int n = 0; n < NK; ++n) {
                     const float2 a = *reinterpret_cast<const float2 *>(N + n * 8);
@@ -558,6 +568,14 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
                     A[n][2] = b.x;
                     A[n][3] = b.y;
                 }
+            }
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+            __syncthreads();   // the transition is here, the last step's stage is read
+            if (i + STAGES < ns)
+                load(i + STAGES - 1);
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+            if (won) {
+                const uint32_t m = sa + i % STAGES * STG;
 #pragma unroll
                 for (int ks = 0; ks < DKP / 16; ++ks) {
                     uint32_t a[3][4];
@@ -590,6 +608,7 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
                         dst[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] = S[n][j];
                 }
         }
+        cp_wait();
         __syncthreads();
     }
 }

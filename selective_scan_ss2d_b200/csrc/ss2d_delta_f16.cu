@@ -1,4 +1,4 @@
-// ss2d_delta_f16.cu -- the gated delta rule's kernels for __half inputs.
+// ss2d_delta_f16.cu -- the gated delta rule's forward kernels for __half inputs.
 #include "ss2d_delta_launch.cuh"
 
 namespace ss2d {

@@ -1,4 +1,4 @@
-// ss2d_delta_f32.cu -- the gated delta rule's kernels for float inputs.
+// ss2d_delta_f32.cu -- the gated delta rule's forward kernels for float inputs.
 #include "ss2d_delta_launch.cuh"
 
 namespace ss2d {

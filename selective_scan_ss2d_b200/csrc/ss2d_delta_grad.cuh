@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                         const int j = bj * 16 + jc + e, x = hf * 2 + e;
                         vp[e] = va[e] = 0.f;
                         if (j <= i) {
-                            const float D = expf((ch[i] - ch[j]) + (cl[i] - cl[j]));
+                            const float D = delta_decay(ch[i] - ch[j], cl[i] - cl[j]);
                             vp[e] = p.scale * D * dP[n][x];
                             float E = vp[e] * qk[n][x];
                             if (j < i) {

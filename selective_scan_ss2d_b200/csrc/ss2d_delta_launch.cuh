@@ -77,13 +77,30 @@ cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
         return launch_out<Tin, DKP, 4, NP, NPP, 1>(p, st);
     return launch_out<Tin, DKP, 4, NP, NPP, two>(p, st);
 }
+template <typename Tin, int DKP, int MODE>
+cudaError_t launch_one(const DeltaParams &p, cudaStream_t st)
+{
+    constexpr int smem = ChainLayout<Tin, DKP, 4, MODE, 3, 3, 1>::bytes;
+    auto kern = delta_one_kernel<Tin, DKP, 4, 1, MODE>;
+    const cudaError_t e = delta_smem(kern, smem);
+    if (e != cudaSuccess)
+        return e;
+    const long long units = delta_units(p);
+    kern<<<dim3((p.DV + 63) / 64, p.H, (unsigned)(units < 65535 ? units : 65535)), 128, smem, st>>>(p, units);
+    return cudaGetLastError();
+}
+// Both chains of a backward pass in one launch while they do not fill the SMs
+// twice; beyond that one after the other: CTAs of both on an SM wait for
+// instructions (6144 chunks of 64 x 64 heads: 3 of 10 cycles a warp waited).
 template <typename Tin, int DKP>
 cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
 {
     const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p) * 2;
+    if (ctas > 2 * 148) {
+        const cudaError_t e = launch_one<Tin, DKP, kChainState>(p, st);
+        return e != cudaSuccess ? e : launch_one<Tin, DKP, kChainRev>(p, st);
+    }
     constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainRev, 3, 3, 2>::bytes);
-    if (two == 1 || ctas > 2 * 148)
-        return launch_both<Tin, DKP, 4, 1>(p, st);
     return launch_both<Tin, DKP, 4, two>(p, st);
 }
 
@@ -105,7 +122,7 @@ cudaError_t launch_segments(const DeltaParams &p, cudaStream_t st)
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    constexpr int csmem = 2 * 3 * DKP * DKP * 2;
+    constexpr int csmem = combine_stages(DKP) * 3 * DKP * DKP * 2;
     auto comb = delta_combine_kernel<DKP, REV>;
     e = delta_smem(comb, csmem);
     if (e != cudaSuccess)
@@ -156,15 +173,22 @@ cudaError_t launch_fwd(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t s
         return pl.np == 3 ? launch_fwd_parts<Tin, DKP, 3, 2>(p, st) : launch_fwd_parts<Tin, DKP, 2, 2>(p, st);
 }
 
-// Columns of a state per CTA: 128 (or all), fewer while that leaves SMs without work.
+// Columns of a state per CTA: 64 (or all), fewer while that leaves SMs without
+// work.  CTAs of 128 columns (16 rows of four to a thread, two CTAs per SM) took
+// 123 us for 4096 states of 128 x 128.
 template <typename Tin>
 cudaError_t launch_recur(const DeltaParams &p, cudaStream_t st)
 {
-    int dvt = p.DV < 128 ? p.DV : 128;
+    int dvt = p.DV < 64 ? p.DV : 64;
     while (dvt > 16 && dvt % 32 == 0 && (long long)((p.DV + dvt - 1) / dvt) * p.H * p.nseq < 148)
         dvt /= 2;
     const dim3 grid((p.DV + dvt - 1) / dvt, p.H, p.nseq < 65535 ? p.nseq : 65535);
-    delta_recur_kernel<Tin><<<grid, kRecurThreads, 0, st>>>(p, dvt);
+    // rows per thread: DK over the row groups of 256 threads
+    const int rows = (p.DK + kRecurThreads / (dvt / 4) - 1) / (kRecurThreads / (dvt / 4));
+    if (rows <= 4)
+        delta_recur_kernel<Tin, 4><<<grid, kRecurThreads, 0, st>>>(p, dvt);
+    else
+        delta_recur_kernel<Tin, 8><<<grid, kRecurThreads, 0, st>>>(p, dvt);
     return cudaGetLastError();
 }
 
@@ -173,8 +197,11 @@ cudaError_t launch_delta(const DeltaParams &p, const DeltaPlan &pl, int what, cu
 {
     if (what == kDeltaRecur)
         return launch_recur<Tin>(p, st);
-    if (what == kDeltaFwd)
-        return pl.dkp == 64 ? launch_fwd<Tin, 64>(p, pl, st) : launch_fwd<Tin, 128>(p, pl, st);
+    return pl.dkp == 64 ? launch_fwd<Tin, 64>(p, pl, st) : launch_fwd<Tin, 128>(p, pl, st);
+}
+template <typename Tin>
+cudaError_t launch_delta_bwd(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st)
+{
     return pl.dkp == 64 ? launch_bwd<Tin, 64>(p, st) : launch_bwd<Tin, 128>(p, st);
 }
 

@@ -15,10 +15,13 @@ struct DeltaPlan {
     int np, npp;   // parts of T, of P
 };
 
+// what: the recurrent kernel or the chunked forward
+enum { kDeltaRecur = 0, kDeltaFwd = 1, kDeltaBwd = 2 };
 cudaError_t launch_delta_bf16(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st);
 cudaError_t launch_delta_f16(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st);
 cudaError_t launch_delta_f32(const DeltaParams &p, const DeltaPlan &pl, int what, cudaStream_t st);
-// what: the recurrent kernel, the chunked forward, the backward
-enum { kDeltaRecur = 0, kDeltaFwd = 1, kDeltaBwd = 2 };
+cudaError_t launch_delta_bwd_bf16(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st);
+cudaError_t launch_delta_bwd_f16(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st);
+cudaError_t launch_delta_bwd_f32(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st);
 
 }  // namespace ss2d
