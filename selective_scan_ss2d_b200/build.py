@@ -19,11 +19,13 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libss2d_b200.so")
 SOURCES = ["ss2d_capi.cu", "ss2d_launch.cu", "ss2d_noalloc.cu", "ss2d_scan_bf16.cu",
            "ss2d_scan_f32.cu", "ss2d_scan_f16.cu", "ss2d_backward.cu", "ss2d_front.cu",
-           "ss2d_norm.cu", "ss2d_delta.cu", "ss2d_delta_bf16.cu", "ss2d_delta_f16.cu",
+           "ss2d_norm.cu", "ss2d_norm_bf16.cu", "ss2d_norm_f16.cu", "ss2d_norm_f32.cu",
+           "ss2d_delta.cu", "ss2d_delta_bf16.cu", "ss2d_delta_f16.cu",
            "ss2d_delta_f32.cu", "ss2d_delta_bwd_bf16.cu", "ss2d_delta_bwd_f16.cu",
            "ss2d_delta_bwd_f32.cu"]
 HEADERS = ["ss2d_kernels.cuh", "ss2d_scan.cuh", "ss2d_front.cuh", "ss2d_scan_launch.cuh", "ss2d_launch.h",
-           "ss2d_params.h", "ss2d_backward.cuh", "ss2d_bwd_params.h", "ss2d_norm.cuh", "ss2d_delta.cuh",
+           "ss2d_params.h", "ss2d_backward.cuh", "ss2d_bwd_params.h", "ss2d_norm.cuh", "ss2d_norm_launch.h",
+           "ss2d_norm_launch.cuh", "ss2d_delta.cuh",
            "ss2d_delta_chain.cuh", "ss2d_delta_grad.cuh", "ss2d_delta_launch.cuh", "ss2d_delta_launch.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -6,7 +6,7 @@
 
 #include "ss2d.h"
 #include "ss2d_launch.h"
-#include "ss2d_norm.cuh"
+#include "ss2d_norm_launch.h"
 
 namespace {
 
@@ -68,63 +68,55 @@ int check(const void *const *need, int nneed, const void *const *opt, int nopt, 
     return SS2D_OK;
 }
 
-// vectors of 16 bytes where every row of every tensor starts on a 16-byte
-// boundary, single values otherwise
-bool vector_rows(const NormCall &c)
+// Vectors where every row of every tensor starts on a 16-byte boundary, single
+// values otherwise; E values a thread, in teams of the smallest power of two that
+// holds a row.  Rows that fill their teams, of 8 * 2^k values or 12 * 2^k (a width of 192
+// in teams of 16, not of 32 with a quarter idle), have kernels for the combinations
+// that blocks are made of: a norm with or without its gate, a residual, alone or
+// scaled and with biases, with the next norm, all of a block; the others look up what
+// they have.
+ss2d::NormPlan norm_plan(NormCall &c, bool bwd)
 {
+    using namespace ss2d;
+    NormParams &p = c.p;
     const int esz = c.dtype == SS2D_F32 ? 4 : 2;
-    return c.p.D % 8 == 0 && c.p.xs * esz % 16 == 0 && (!c.p.z || c.p.zs * esz % 16 == 0);
-}
-
-// Threads of a row's team: the smallest power of two that holds the row at E
-// values a thread.
-int team_size(int D, int E)
-{
-    int t = 1;
-    while (t * E < D)
-        t <<= 1;
-    return t;
-}
-
-template <typename Tin, typename Tr, int V, int E>
-cudaError_t launch(const NormCall &c, bool bwd, int grid, int threads, cudaStream_t st)
-{
-    if (bwd) {
-        const size_t smem = sizeof(float) * threads * E;
-        if (c.p.cols >> 3)
-            ss2d::norm_bwd_kernel<Tin, Tr, V, E, true><<<grid, threads, smem, st>>>(c.p);
-        else
-            ss2d::norm_bwd_kernel<Tin, Tr, V, E, false><<<grid, threads, smem, st>>>(c.p);
-    } else {
-        ss2d::norm_fwd_kernel<Tin, Tr, V, E><<<grid, threads, 0, st>>>(c.p);
+    const bool vec = p.D % 8 == 0 && p.xs * esz % 16 == 0 && (!p.z || p.zs * esz % 16 == 0);
+    NormPlan pl{vec ? 8 : 1, p.D <= 4096 ? 8 : 16, kNormAny};
+    auto team = [&](int E) {
+        int t = 1;
+        while (t * E < p.D)
+            t <<= 1;
+        return t;
+    };
+    if (vec && p.D <= 4096) {
+        // in the backward pass r is r', which the second norm reads; the residual itself costs nothing
+        const bool res = bwd ? p.pre != kNormNone : p.r != nullptr;
+        const bool bias = (p.post && p.b_post) || (p.pre && p.b_pre) || p.cols >> 3;
+        const int has = (p.post ? kHasPost : 0) | (p.z ? kHasGate : 0) | (res ? kHasRes : 0) |
+                        (p.pre ? kHasPre : 0) | (p.s ? kHasScale : 0) | (bias ? kHasBias : 0);
+        const bool known = has == kHasPost || has == (kHasPost | kHasGate) || has == (kHasRes | kHasPre) ||
+                           has == (kHasRes | kHasPre | kHasScale | kHasBias) ||
+                           has == (kHasPost | kHasGate | kHasRes | kHasPre | kHasScale);
+        if (known && team(8) * 8 == p.D) {
+            pl.M = has;
+        } else if (known && team(12) * 12 == p.D) {
+            pl = NormPlan{4, 12, has};
+        }
     }
-    return cudaGetLastError();
+    p.tpr = team(pl.E);
+    return pl;
 }
 
-template <typename Tin, typename Tr>
-cudaError_t launch_type(const NormCall &c, bool bwd, int grid, int threads, bool vec, cudaStream_t st)
+cudaError_t launch_norm(const NormCall &c, const ss2d::NormPlan &pl, bool bwd, int grid, int threads, cudaStream_t st)
 {
-    constexpr int V = 8;   // one 16-byte vector of 16-bit values, two of float32
-    if (c.p.D <= 4096)
-        return vec ? launch<Tin, Tr, V, 8>(c, bwd, grid, threads, st)
-                   : launch<Tin, Tr, 1, 8>(c, bwd, grid, threads, st);
-    return vec ? launch<Tin, Tr, V, 16>(c, bwd, grid, threads, st)
-               : launch<Tin, Tr, 1, 16>(c, bwd, grid, threads, st);
-}
-
-cudaError_t launch_norm(const NormCall &c, bool bwd, int grid, int threads, cudaStream_t st)
-{
-    const bool vec = vector_rows(c);
     const bool rf = c.r_dtype == SS2D_F32;
     switch (c.dtype) {
     case SS2D_F32:
-        return launch_type<float, float>(c, bwd, grid, threads, vec, st);
+        return ss2d::launch_norm_f32(c.p, pl, bwd, grid, threads, st);
     case SS2D_BF16:
-        return rf ? launch_type<__nv_bfloat16, float>(c, bwd, grid, threads, vec, st)
-                  : launch_type<__nv_bfloat16, __nv_bfloat16>(c, bwd, grid, threads, vec, st);
+        return ss2d::launch_norm_bf16(c.p, pl, bwd, rf, grid, threads, st);
     default:
-        return rf ? launch_type<__half, float>(c, bwd, grid, threads, vec, st)
-                  : launch_type<__half, __half>(c, bwd, grid, threads, vec, st);
+        return ss2d::launch_norm_f16(c.p, pl, bwd, rf, grid, threads, st);
     }
 }
 
@@ -167,12 +159,12 @@ int block_norm_fwd(const void *x, const void *z, const void *r, const float *s, 
     rc = check(need, 3, opt, 7, c);
     if (rc != SS2D_OK)
         return rc;
-    p.tpr = team_size(D, D <= 4096 ? 8 : 16);
+    const ss2d::NormPlan pl = norm_plan(c, false);
     const int threads = p.tpr > 256 ? p.tpr : 256;
     const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
     // four CTAs of 256 threads at the kernel's registers fill an SM
     const int grid = ctas > 148 * 4 ? 148 * 4 : (int)ctas;
-    const cudaError_t e = launch_norm(c, false, grid, threads, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_norm(c, pl, false, grid, threads, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
         ss2d::record_error("kernel launch", e);
         return SS2D_ERR_CUDA;
@@ -239,8 +231,7 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
         return rc;
     if (!z)
         p.dz = nullptr;
-    const int E = D <= 4096 ? 8 : 16;
-    p.tpr = team_size(D, E);
+    const ss2d::NormPlan pl = norm_plan(c, true);
     const int threads = p.tpr > 256 ? p.tpr : 256;
     const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
     // two CTAs of 256 threads at the kernel's registers fill an SM; more CTAs only add partials
@@ -252,10 +243,9 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
             return rc;
     }
     p.part = static_cast<float *>(part);
-    e = launch_norm(c, true, grid, threads, st);
+    e = launch_norm(c, pl, true, grid, threads, st);
     if (e == cudaSuccess && p.cols) {
-        ss2d::norm_colsum_kernel<<<dim3((D + 31) / 32, ss2d::kNormCols), 1024, 0, st>>>(p.part, out, grid, D);
-        e = cudaGetLastError();
+        e = ss2d::launch_norm_colsum(p.part, out, grid, D, st);
     }
     cudaError_t ef = cudaSuccess;
     if (part)

@@ -57,31 +57,40 @@ struct NormParams {
 };
 
 // Thread t of a team holds vectors t, t + TPR, ... of V values of a row; a
-// vector is 16 bytes of 16-bit values, two 16-byte pieces of float32, or (V = 1)
-// one value.  Rows are loaded as stored and converted when they are used, so that
+// vector is 16 bytes of 16-bit values (8: V = 4), one or two 16-byte pieces of
+// float32, or (V = 1) one value.  Rows are loaded as stored and converted when they are used, so that
 // the next row can be on its way at half the registers.
 template <typename T, int V>
 struct NormVec {
-    static constexpr int n = V == 1 ? 1 : V * (int)sizeof(T) / 16;
-    typename std::conditional<V == 1, T, uint4>::type w[n];
+    static constexpr int bytes = V * (int)sizeof(T), n = V == 1 ? 1 : bytes / 4;
+    typename std::conditional<V == 1, T, uint32_t>::type w[n];
     __device__ __forceinline__ void load(const T *row, int col)
     {
         if constexpr (V == 1) {
             w[0] = row[col];
+        } else if constexpr (bytes == 8) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(row + col);
+            w[0] = u.x;
+            w[1] = u.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < n; ++i)
-                w[i] = reinterpret_cast<const uint4 *>(row + col)[i];
+            for (int i = 0; i < n / 4; ++i) {
+                const uint4 u = reinterpret_cast<const uint4 *>(row + col)[i];
+                w[4 * i] = u.x;
+                w[4 * i + 1] = u.y;
+                w[4 * i + 2] = u.z;
+                w[4 * i + 3] = u.w;
+            }
         }
     }
     __device__ __forceinline__ void zero()
     {
-        if constexpr (V == 1) {
-            w[0] = T(0.f);
-        } else {
 #pragma unroll
-            for (int i = 0; i < n; ++i)
-                w[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < n; ++i) {
+            if constexpr (V == 1)
+                w[i] = T(0.f);
+            else
+                w[i] = 0;
         }
     }
     __device__ __forceinline__ void get(float *v) const
@@ -91,15 +100,11 @@ struct NormVec {
         } else {
 #pragma unroll
             for (int i = 0; i < n; ++i) {
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(T) == 4) {
-                        v[4 * i + j] = __uint_as_float(u[j]);
-                    } else {
-                        v[8 * i + 2 * j] = half_bits_to_f32<T>(u[j] & 0xffffu);
-                        v[8 * i + 2 * j + 1] = half_bits_to_f32<T>(u[j] >> 16);
-                    }
+                if constexpr (sizeof(T) == 4) {
+                    v[i] = __uint_as_float(w[i]);
+                } else {
+                    v[2 * i] = half_bits_to_f32<T>(w[i] & 0xffffu);
+                    v[2 * i + 1] = half_bits_to_f32<T>(w[i] >> 16);
                 }
             }
         }
@@ -116,13 +121,13 @@ __device__ __forceinline__ void norm_load(const T *row, int col, float *v)
 template <typename T, int V, int E>
 struct NormRow {
     NormVec<T, V> v[E / V];
-    template <typename Col>
-    __device__ __forceinline__ void load(const T *row, bool live, int D, Col col)
+    template <typename On, typename Col>
+    __device__ __forceinline__ void load(const T *row, bool live, On on, Col col)
     {
 #pragma unroll
         for (int i = 0; i < E / V; ++i) {
             v[i].zero();
-            if (live && col(i) < D)
+            if (live && on(i))
                 v[i].load(row, col(i));
         }
     }
@@ -153,11 +158,14 @@ __device__ __forceinline__ void norm_store(T *row, int col, const float *v)
         for (int i = 0; i < V; i += 4)
             *reinterpret_cast<float4 *>(row + col + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     } else {
-        __align__(16) T h[8];
+        __align__(16) T h[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < V; ++i)
             h[i] = norm_round<T>(v[i]);
-        *reinterpret_cast<uint4 *>(row + col) = *reinterpret_cast<const uint4 *>(h);
+        if constexpr (V == 8)
+            *reinterpret_cast<uint4 *>(row + col) = *reinterpret_cast<const uint4 *>(h);
+        else
+            *reinterpret_cast<uint2 *>(row + col) = *reinterpret_cast<const uint2 *>(h);
     }
 }
 
@@ -332,35 +340,90 @@ __device__ __forceinline__ void norm_grad(float (&d)[E], const float (&n)[E], fl
         d[e] = in(e) ? rs * (d[e] - n[e] * ma - mb) : 0.f;
 }
 
+// What a call has, as kernels are compiled for: the parts below, for rows that fill
+// their teams (D = TPR * E), or kNormAny: whatever the parameters say.  With every part
+// looked up and every column compared in the loop, the gated norm of 302592 rows of 64
+// values issued 35 instructions a value and took 29 us, at 72 % of the issue slots.
+enum { kHasPost = 1, kHasGate = 2, kHasRes = 4, kHasPre = 8, kHasScale = 16, kHasBias = 32, kNormAny = -1 };
+
 // grid: CTAs of blockDim.x / tpr teams, one row per team and step; the next
-// row's vectors are loaded as soon as this row's are converted.  Measured without
-// that, one row per team at a time: the gated norm of 302592 rows of 64 values 49 us.
-template <typename Tin, typename Tr, int V, int E>
+// row's vectors are loaded as soon as this row's are converted, and a compiled
+// combination keeps its weights in registers.
+template <typename Tin, typename Tr, int V, int E, int M>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
 {
     __shared__ float2 red[64];
+    constexpr bool any = M == kNormAny;
+    const bool post = any ? p.post != kNormNone : M & kHasPost, gate = any ? p.z != nullptr : M & kHasGate,
+               res = any ? p.r != nullptr : M & kHasRes, pre = any ? p.pre != kNormNone : M & kHasPre,
+               scale = any ? p.s != nullptr : M & kHasScale, bias = any || (M & kHasBias);
     const int lane = threadIdx.x % p.tpr, team = threadIdx.x / p.tpr, teams = blockDim.x / p.tpr;
     const int D = p.D;
     auto col = [&](int i) { return (lane + i * p.tpr) * V; };   // first column of vector i
-    auto in = [&](int e) { return (lane + e / V * p.tpr) * V + e % V < D; };
+    auto on = [&](int i) { return !any || col(i) < D; };
+    auto in = [&](int e) { return !any || (lane + e / V * p.tpr) * V + e % V < D; };
     TeamSum sum;
     sum.init(red, p.tpr);
+    // f(w, i): weights of vector i, from registers in a compiled combination
+    constexpr int K = any ? 1 : E;
+    float wq[K], wp[K], ws[K];
+    auto keep = [&](const float *src, bool has, float (&w)[K]) {
+        if constexpr (!any) {
+            if (has) {
+#pragma unroll
+                for (int i = 0; i < E / V; ++i) {
+                    if (src) {
+                        norm_load<float, V>(src, col(i), w + i * V);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            w[i * V + j] = 1.f;
+                    }
+                }
+            }
+        }
+    };
+    keep(p.w_post, post, wq);
+    keep(p.w_pre, pre, wp);
+    keep(p.s, scale, ws);
+    auto times = [&](float *v, int i, const float *src, const float (&w)[K]) {
+        if constexpr (!any) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] *= w[i * V + j];
+        } else if (src) {
+            float t[V];
+            norm_load<float, V>(src, col(i), t);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] *= t[j];
+        }
+    };
+    auto plus = [&](float *v, int i, const float *src) {
+        if (bias && src) {
+            float t[V];
+            norm_load<float, V>(src, col(i), t);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] += t[j];
+        }
+    };
     const long long step = (long long)gridDim.x * teams;
     NormRow<Tin, V, E> xr, zr;
     NormRow<Tr, V, E> rr;
     auto load_x = [&](long long o) {
         const bool live = o < p.rows;
-        xr.load(static_cast<const Tin *>(p.x) + (live ? norm_row(o, p.group, p.xs, D) : 0), live, D, col);
+        xr.load(static_cast<const Tin *>(p.x) + (live ? norm_row(o, p.group, p.xs, D) : 0), live, on, col);
     };
     auto load_z = [&](long long o) {
         const bool live = o < p.rows;
-        if (p.z)
-            zr.load(static_cast<const Tin *>(p.z) + (live ? norm_row(o, p.group, p.zs, D) : 0), live, D, col);
+        if (gate)
+            zr.load(static_cast<const Tin *>(p.z) + (live ? norm_row(o, p.group, p.zs, D) : 0), live, on, col);
     };
     auto load_r = [&](long long o) {
         const bool live = o < p.rows;
-        if (p.r)
-            rr.load(static_cast<const Tr *>(p.r) + (live ? o * D : 0), live, D, col);
+        if (res)
+            rr.load(static_cast<const Tr *>(p.r) + (live ? o * D : 0), live, on, col);
     };
     const long long first = (long long)blockIdx.x * teams;
     load_x(first + team);
@@ -372,45 +435,29 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
         float v[E], w[E];
         xr.get(v);
         load_x(o + step);
-        if (p.post != kNormNone) {
+        if (post) {
             norm_rows<E>(v, p.post, D, p.eps, sum, in);
 #pragma unroll
-            for (int i = 0; i < E / V; ++i) {
-                if (col(i) >= D)
-                    continue;
-                if (p.w_post) {
-                    norm_load<float, V>(p.w_post, col(i), w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        v[i * V + j] *= w[j];
+            for (int i = 0; i < E / V; ++i)
+                if (on(i)) {
+                    times(v + i * V, i, p.w_post, wq);
+                    plus(v + i * V, i, p.b_post);
                 }
-                if (p.b_post) {
-                    norm_load<float, V>(p.b_post, col(i), w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        v[i * V + j] += w[j];
-                }
-            }
         }
-        if (p.z) {
+        if (gate) {
             zr.get(w);
             load_z(o + step);
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 v[e] *= w[e] * norm_sigmoid(w[e]);
         }
-        if (p.s) {
+        if (scale) {
 #pragma unroll
-            for (int i = 0; i < E / V; ++i) {
-                if (col(i) >= D)
-                    continue;
-                norm_load<float, V>(p.s, col(i), w);
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[i * V + j] *= w[j];
-            }
+            for (int i = 0; i < E / V; ++i)
+                if (on(i))
+                    times(v + i * V, i, p.s, ws);
         }
-        if (p.r) {
+        if (res) {
             rr.get(w);
             load_r(o + step);
 #pragma unroll
@@ -419,30 +466,19 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
         }
 #pragma unroll
         for (int i = 0; i < E / V; ++i)
-            if (live && col(i) < D)
+            if (live && on(i))
                 norm_store<Tr, V>(static_cast<Tr *>(p.r_out) + o * D, col(i), v + i * V);
-        if (p.pre != kNormNone) {
+        if (pre) {
             // the norm reads r' before its rounding to r's type
             norm_rows<E>(v, p.pre, D, p.eps, sum, in);
 #pragma unroll
-            for (int i = 0; i < E / V; ++i) {
-                if (col(i) >= D)
-                    continue;
-                if (p.w_pre) {
-                    norm_load<float, V>(p.w_pre, col(i), w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        v[i * V + j] *= w[j];
+            for (int i = 0; i < E / V; ++i)
+                if (on(i)) {
+                    times(v + i * V, i, p.w_pre, wp);
+                    plus(v + i * V, i, p.b_pre);
+                    if (live)
+                        norm_store<Tin, V>(static_cast<Tin *>(p.y) + o * D, col(i), v + i * V);
                 }
-                if (p.b_pre) {
-                    norm_load<float, V>(p.b_pre, col(i), w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        v[i * V + j] += w[j];
-                }
-                if (live)
-                    norm_store<Tin, V>(static_cast<Tin *>(p.y) + o * D, col(i), v + i * V);
-            }
         }
     }
 }
@@ -452,17 +488,22 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
 // vectors are on their way while a row's sums go round, and both norms' statistics
 // go round together: with loads where they are used and every sum by itself,
 // 12544 rows of 1024 values with every part took 144 us.
-template <typename Tin, typename Tr, int V, int E, bool BIAS>
+template <typename Tin, typename Tr, int V, int E, bool BIAS, int M>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
 {
     constexpr int NC = BIAS ? kNormCols : 3;
-    constexpr bool ahead = E == 8;   // rows of 4097 values and more have no registers for it
+    constexpr bool ahead = E < 16;   // rows of 4097 values and more have no registers for it
     extern __shared__ __align__(16) float csum[];
     __shared__ float2 red[64];
     const int lane = threadIdx.x % p.tpr, team = threadIdx.x / p.tpr, teams = blockDim.x / p.tpr;
+    constexpr bool any = M == kNormAny;
+    const bool post = any ? p.post != kNormNone : M & kHasPost, gate = any ? p.z != nullptr : M & kHasGate,
+               pre = any ? p.pre != kNormNone : M & kHasPre, scale = any ? p.s != nullptr : M & kHasScale,
+               bias = any || (M & kHasBias);
     const int D = p.D;
     auto col = [&](int i) { return (lane + i * p.tpr) * V; };
-    auto in = [&](int e) { return (lane + e / V * p.tpr) * V + e % V < D; };
+    auto on = [&](int i) { return !any || col(i) < D; };
+    auto in = [&](int e) { return !any || (lane + e / V * p.tpr) * V + e % V < D; };
     TeamSum sum;
     sum.init(red, p.tpr);
     float acc[NC][E];
@@ -485,24 +526,24 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
     NormRow<Tr, V, E> rr, gr;
     auto row_x = [&](long long o) {
         const bool live = o < p.rows;
-        xr.load(static_cast<const Tin *>(p.x) + (live ? norm_row(o, p.group, p.xs, D) : 0), live, D, col);
+        xr.load(static_cast<const Tin *>(p.x) + (live ? norm_row(o, p.group, p.xs, D) : 0), live, on, col);
     };
     auto row_z = [&](long long o) {
         const bool live = o < p.rows;
-        if (p.z)
-            zr.load(static_cast<const Tin *>(p.z) + (live ? norm_row(o, p.group, p.zs, D) : 0), live, D, col);
+        if (gate)
+            zr.load(static_cast<const Tin *>(p.z) + (live ? norm_row(o, p.group, p.zs, D) : 0), live, on, col);
     };
     auto row_pre = [&](long long o) {
         const bool live = o < p.rows;
-        if (p.pre != kNormNone) {
-            rr.load(static_cast<const Tr *>(p.r) + (live ? o * D : 0), live, D, col);
-            yr.load(static_cast<const Tin *>(p.dy) + (live ? o * D : 0), live, D, col);
+        if (pre) {
+            rr.load(static_cast<const Tr *>(p.r) + (live ? o * D : 0), live, on, col);
+            yr.load(static_cast<const Tin *>(p.dy) + (live ? o * D : 0), live, on, col);
         }
     };
     auto row_g = [&](long long o) {
         const bool live = o < p.rows;
         if (p.dr_out)
-            gr.load(static_cast<const Tr *>(p.dr_out) + (live ? o * D : 0), live, D, col);
+            gr.load(static_cast<const Tr *>(p.dr_out) + (live ? o * D : 0), live, on, col);
     };
     const long long first = (long long)blockIdx.x * teams;
     if constexpr (ahead) {
@@ -526,10 +567,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
         }
         // both norms' statistics in one round of sums
         float2 mean, rs;
-        norm_stats2<E>([&](float (&v)[E]) { rr.get(v); }, p.pre, [&](float (&v)[E]) { xr.get(v); }, p.post, D, p.eps,
+        norm_stats2<E>([&](float (&v)[E]) { rr.get(v); }, pre ? p.pre : kNormNone,
+                       [&](float (&v)[E]) { xr.get(v); }, post ? p.post : kNormNone, D, p.eps,
                        sum, in, mean, rs);
         // G: the gradient of r'
-        if (p.pre != kNormNone) {
+        if (pre) {
             rr.get(a);
             yr.get(g);
             if constexpr (ahead)
@@ -540,7 +582,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
 #pragma unroll
             for (int i = 0; i < E / V; ++i) {
                 float w[V];
-                if (col(i) < D)
+                if (on(i))
                     vec(p.w_pre, i, 1.f, w);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -548,7 +590,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
                     acc[2][e] = fmaf(g[e], a[e], acc[2][e]);
                     if constexpr (BIAS)
                         acc[4][e] += g[e];
-                    g[e] = col(i) < D ? g[e] * w[j] : 0.f;
+                    g[e] = on(i) ? g[e] * w[j] : 0.f;
                 }
             }
             norm_grad<E>(g, a, rs.x, p.pre, D, sum, in);
@@ -564,61 +606,61 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
         if (p.dr) {
 #pragma unroll
             for (int i = 0; i < E / V; ++i)
-                if (live && col(i) < D)
+                if (live && on(i))
                     norm_store<Tr, V>(static_cast<Tr *>(p.dr) + o * D, col(i), g + i * V);
         }
         // the branch again: n, p, t
         xr.get(a);
         if constexpr (ahead)
             row_x(o + step);
-        if (p.post != kNormNone) {
+        if (post) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 a[e] = in(e) ? (a[e] - mean.y) * rs.y : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < E / V; ++i) {
-            const bool on = col(i) < D;
             float w[V], b[V], s[V], z[V], dz[V];
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 w[j] = b[j] = s[j] = z[j] = 0.f;
-            if (on) {
-                vec(p.post != kNormNone ? p.w_post : nullptr, i, 1.f, w);
-                vec(p.post != kNormNone ? p.b_post : nullptr, i, 0.f, b);
-                vec(p.s, i, 1.f, s);
+            if (on(i)) {
+                vec(post ? p.w_post : nullptr, i, 1.f, w);
+                vec(post && bias ? p.b_post : nullptr, i, 0.f, b);
+                vec(scale ? p.s : nullptr, i, 1.f, s);
             }
-            if (p.z)
+            if (gate)
                 zr.v[i].get(z);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int e = i * V + j;
                 const float pv = fmaf(a[e], w[j], b[j]);
-                float gate = 1.f, dgate = 0.f;
-                if (p.z) {
+                float gt = 1.f, dgate = 0.f;
+                if (gate) {
                     const float sg = norm_sigmoid(z[j]);
-                    gate = z[j] * sg;
+                    gt = z[j] * sg;
                     dgate = sg * fmaf(z[j], 1.f - sg, 1.f);
                 }
-                acc[0][e] = fmaf(g[e], pv * gate, acc[0][e]);
+                if (scale)
+                    acc[0][e] = fmaf(g[e], pv * gt, acc[0][e]);
                 const float dt = s[j] * g[e];
                 dz[j] = dt * pv * dgate;
-                const float dp = dt * gate;
+                const float dp = dt * gt;
                 acc[1][e] = fmaf(dp, a[e], acc[1][e]);
                 if constexpr (BIAS)
                     acc[3][e] += dp;
                 g[e] = dp * w[j];
             }
-            if (p.dz && live && on)
+            if (gate && p.dz && live && on(i))
                 norm_store<Tin, V>(static_cast<Tin *>(p.dz) + o * D, col(i), dz);
         }
         if constexpr (ahead)
             row_z(o + step);
-        if (p.post != kNormNone)
+        if (post)
             norm_grad<E>(g, a, rs.y, p.post, D, sum, in);
 #pragma unroll
         for (int i = 0; i < E / V; ++i)
-            if (live && col(i) < D)
+            if (live && on(i))
                 norm_store<Tin, V>(static_cast<Tin *>(p.dx) + o * D, col(i), g + i * V);
     }
     // the CTA's column sums, its teams in order

@@ -175,7 +175,7 @@ def rowmax(*arrays):
     return sum(np.abs(v).max(-1, keepdims=True) for v in arrays if v is not None)
 
 
-SHAPES = [(1, 1), (3, 5), (7, 8), (9, 64), (33, 96), (65, 191), (130, 192), (17, 384), (5, 1000), (12, 1024),
+SHAPES = [(1, 1), (70, 96), (41, 768), (3, 5), (7, 8), (9, 64), (33, 96), (65, 191), (130, 192), (17, 384), (5, 1000), (12, 1024),
           (6, 4096), (3, 4100), (2, 8192)]
 
 
@@ -193,6 +193,8 @@ def test_forward_and_backward_match_oracle(rows, D, dtype, rdt):
                                                  (True, False, False, True), (False, True, True, False)])
 def test_every_combination_of_parts(post, pre, gate, res, scale, bias):
     check(make(37, 72, post, pre, gate, res, scale, bias), "bf16", "f32" if res else "bf16")
+    check(make(29, 64, post, pre, gate, res, scale, bias), "f16", "f16")    # rows that fill their teams
+    check(make(21, 192, post, pre, gate, res, scale, bias), "bf16", "bf16")
     check(make(11, 45, post, pre, gate, res, scale, bias), "f32", "f32")
 
 
