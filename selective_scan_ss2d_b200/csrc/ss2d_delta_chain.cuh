@@ -66,7 +66,24 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
     const int h = blockIdx.y, hk = h / (p.H / p.HK);
     const int dvw = (tile * NW + warp) * 16;   // first of the warp's DV columns
     const bool won = dvw < (LOCAL && ident ? p.DK : p.DV);
-    for (long long unit = blockIdx.z; unit < units; unit += gridDim.z) {
+    __shared__ int ranked;
+    for (long long z = blockIdx.z; z < units; z += gridDim.z) {
+        // packed sequences are taken by length, the longest first: the last chains to start are short ones
+        long long unit = z;
+        if (p.cu && !p.SC && p.nseq <= NT) {
+            if (tid < p.nseq) {
+                const int len = delta_seq(p, tid).len;
+                int before = 0;
+                for (int i = 0; i < p.nseq; ++i) {
+                    const int l = delta_seq(p, i).len;
+                    before += l > len || (l == len && i < tid);
+                }
+                if (before == (int)z)
+                    ranked = tid;
+            }
+            __syncthreads();
+            unit = ranked;
+        }
         int sn, c0, c1;
         DeltaSeq q;
         if (!delta_unit(p, unit, sn, q, c0, c1))
