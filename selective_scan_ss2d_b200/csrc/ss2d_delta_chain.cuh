@@ -516,22 +516,35 @@ __global__ void __launch_bounds__(128, 2) delta_local_kernel(const DeltaParams p
         delta_chain<Tin, DKP, 4, kChainRev, NP, 3, STAGES, true>(p, x - dvt - dkt, false, units);
 }
 
-__host__ __device__ constexpr int combine_stages(int dkp) { return dkp == 64 ? 4 : 2; }
 // The states that the segments of a sequence start from (blockIdx.x even: dS that
-// they end with): S <- M S + N over them, transposed, a warp 16 columns of DV as in
-// the chain.  One step is DKP^2 products of three parts a column; the next
-// transition is copied meanwhile.  Sequences of no tokens pass their state on.
+// they end with): S <- M S + N over them, transposed, 16 columns of DV to a CTA, a
+// warp 16 of the result's columns.  One step is DKP^2 products of three parts a column;
+// a warp leaves the parts of its columns in shared memory, where all read the next
+// step's A operand.  The next transitions are copied meanwhile.  Steps follow one
+// another, so they are spread over SMs: with 64 columns of DV to a CTA and S kept in
+// a warp's registers a step of 64 x 64 took 2.3 us.  Sequences of no tokens pass their
+// state on.
+template <int DKP>
+struct CombineLayout {
+    static constexpr int stages = DKP == 64 ? 4 : 2;
+    static constexpr int RB = DKP * 2, PB = DKP * RB, STG = 3 * PB;   // a row, a part, a transition
+    static constexpr int SP = 16 * RB;                       // one part of S^T
+    static constexpr int oS = stages * STG;                  // two buffers of S^T
+    static constexpr int bytes = oS + 2 * 3 * SP;
+    static constexpr int threads = DKP * 2;
+};
+
 template <int DKP, bool REV>
-__global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(CombineLayout<DKP>::threads) delta_combine_kernel(const DeltaParams p)
 {
-    constexpr int RB = DKP * 2, PB = DKP * RB, NK = DKP / 8, STG = 3 * PB, STAGES = combine_stages(DKP);
+    using Lay = CombineLayout<DKP>;
+    constexpr int RB = Lay::RB, PB = Lay::PB, STG = Lay::STG, STAGES = Lay::stages, NH = 2;
     extern __shared__ __align__(128) unsigned char dsm[];
     const uint32_t sa = smem_addr(dsm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t2 = (lane & 3) * 2;
     const int h = blockIdx.y, tile = REV ? blockIdx.x >> 1 : blockIdx.x;
     const bool rev = REV && !(blockIdx.x & 1);
-    const int dvw = (tile * 4 + warp) * 16;
-    const bool won = dvw < p.DV;
+    const int dvw = tile * 16, dk0 = warp * 16;
     for (int sn = blockIdx.z; sn < p.nseq; sn += gridDim.z) {
         const DeltaSeq q = delta_seq(p, sn);
         const int nc = (q.len + kDeltaC - 1) / kDeltaC, ns = (nc + p.SC - 1) / p.SC;
@@ -539,21 +552,21 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
         auto seg = [&](int i) { return (u0 + (rev ? ns - 1 - i : i)) * p.H + h; };
         auto load = [&](int i) {
             const char *src = static_cast<const char *>(p.Ms) + seg(i) * STG;
-            for (int k = tid; k < STG / 16; k += 128) {
+            for (int k = tid; k < STG / 16; k += Lay::threads) {
                 const int r = k / (DKP / 8), pc = k % (DKP / 8);   // r counts the parts' rows
                 cp16(sa + i % STAGES * STG + r / DKP * PB + swz<RB>(r % DKP, pc), src + (long long)k * 16,
                      r % DKP < p.DK);
             }
         };
         const float *src = rev ? p.dh_last : p.h0;
-        float S[NK][4];
+        float S[NH][4];
 #pragma unroll
-        for (int n = 0; n < NK; ++n)
+        for (int n = 0; n < NH; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
+                const int dk = dk0 + n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
                 S[n][j] =
-                    src && won && dk < p.DK ? src[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] : 0.f;
+                    src && dk < p.DK ? src[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] : 0.f;
             }
         // one group of copies for each step, empty past the end
         for (int i = 0; i < STAGES - 1; ++i) {
@@ -562,22 +575,23 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
         for (int i = 0; i < ns; ++i) {
-            const long long o = (seg(i) * p.DV + dvw + g8) * DKP + t2;
-            if (won) {
+            const long long o = (seg(i) * p.DV + dvw + g8) * DKP + dk0 + t2;
+            float A[NH][4];
+            const int sbuf = Lay::oS + (i & 1) * 3 * Lay::SP;
+            {
                 float *dst = (rev ? p.dSin : p.Sin) + o;
 #pragma unroll
-                for (int n = 0; n < NK; ++n) {
+                for (int n = 0; n < NH; ++n) {
                     *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(S[n][0], S[n][1]);
                     *reinterpret_cast<float2 *>(dst + 8 * DKP + n * 8) = make_float2(S[n][2], S[n][3]);
                 }
             }
             if (i + 1 == ns)
                 break;
-            float A[NK][4];
-            if (won) {
+            {
                 const float *N = (rev ? p.dNs : p.Ns) + o;
 #pragma unroll
-                for (int n = 0; n < NK; ++n) {
+                for (int n = 0; n < NH; ++n) {
                     const float2 a = *reinterpret_cast<const float2 *>(N + n * 8);
                     const float2 b = *reinterpret_cast<const float2 *>(N + 8 * DKP + n * 8);
                     A[n][0] = a.x;
@@ -585,42 +599,53 @@ __global__ void __launch_bounds__(128) delta_combine_kernel(const DeltaParams p)
                     A[n][2] = b.x;
                     A[n][3] = b.y;
                 }
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[3];
+                        split2<3>(S[n][2 * e], S[n][2 * e + 1], w);
+#pragma unroll
+                        for (int m = 0; m < 3; ++m)
+                            *reinterpret_cast<uint32_t *>(dsm + sbuf + m * Lay::SP +
+                                                          swz<RB>(g8 + 8 * e, warp * 2 + n) + t2 * 2) = w[m];
+                    }
             }
             asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
-            __syncthreads();   // the transition is here, the last step's stage is read
+            __syncthreads();   // the transition and S are here, the last step's stage is read
             if (i + STAGES < ns)
                 load(i + STAGES - 1);
             asm volatile("cp.async.commit_group;\n" ::: "memory");
-            if (won) {
+            {
                 const uint32_t m = sa + i % STAGES * STG;
 #pragma unroll
                 for (int ks = 0; ks < DKP / 16; ++ks) {
                     uint32_t a[3][4];
-                    frag_a<3>(S[2 * ks], S[2 * ks + 1], a);
-                    if (rev) {
 #pragma unroll
-                        for (int nt = 0; nt < NK; nt += 2)
-                            mma_rows<RB, 3, 3, 3>(A[nt], A[nt + 1], a, m, PB, nt * 8, ks * 2);
-                    } else {
+                    for (int k = 0; k < 3; ++k)
+                        ldsm4(sa + sbuf + k * Lay::SP + swz<RB>(lane & 15, ks * 2 + (lane >> 4)), a[k]);
 #pragma unroll
-                        for (int nt = 0; nt < NK; nt += 2)
-                            mma_cols<RB, 3, 3, 3>(A[nt], A[nt + 1], a, m, PB, ks * 16, nt);
+                    for (int nt = 0; nt < NH; nt += 2) {
+                        if (rev)
+                            mma_rows<RB, 3, 3, 3>(A[nt], A[nt + 1], a, m, PB, dk0 + nt * 8, ks * 2);
+                        else
+                            mma_cols<RB, 3, 3, 3>(A[nt], A[nt + 1], a, m, PB, ks * 16, warp * 2 + nt);
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NK; ++n)
+                for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         S[n][j] = A[n][j];
             }
         }
         float *dst = rev ? p.dh0 : p.h_last;
-        if (ns == 0 && dst && won) {
+        if (ns == 0 && dst) {
 #pragma unroll
-            for (int n = 0; n < NK; ++n)
+            for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int dk = n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
+                    const int dk = dk0 + n * 8 + t2 + (j & 1), dv = dvw + g8 + (j >> 1) * 8;
                     if (dk < p.DK)
                         dst[(((long long)sn * p.H + h) * p.DK + dk) * p.DV + dv] = S[n][j];
                 }

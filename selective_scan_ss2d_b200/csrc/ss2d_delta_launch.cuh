@@ -122,12 +122,12 @@ cudaError_t launch_segments(const DeltaParams &p, cudaStream_t st)
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    constexpr int csmem = combine_stages(DKP) * 3 * DKP * DKP * 2;
+    using CL = CombineLayout<DKP>;
     auto comb = delta_combine_kernel<DKP, REV>;
-    e = delta_smem(comb, csmem);
+    e = delta_smem(comb, CL::bytes);
     if (e != cudaSuccess)
         return e;
-    comb<<<dim3(dvt * (REV ? 2 : 1), p.H, p.nseq < 65535 ? p.nseq : 65535), 128, csmem, st>>>(p);
+    comb<<<dim3(p.DV / 16 * (REV ? 2 : 1), p.H, p.nseq < 65535 ? p.nseq : 65535), CL::threads, CL::bytes, st>>>(p);
     return cudaGetLastError();
 }
 
