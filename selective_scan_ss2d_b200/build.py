@@ -26,7 +26,7 @@ SOURCES = ["ss2d_capi.cu", "ss2d_launch.cu", "ss2d_noalloc.cu", "ss2d_scan_bf16.
 HEADERS = ["ss2d_kernels.cuh", "ss2d_scan.cuh", "ss2d_front.cuh", "ss2d_scan_launch.cuh", "ss2d_launch.h",
            "ss2d_params.h", "ss2d_backward.cuh", "ss2d_bwd_params.h", "ss2d_norm.cuh", "ss2d_norm_launch.h",
            "ss2d_norm_launch.cuh", "ss2d_delta.cuh",
-           "ss2d_delta_chain.cuh", "ss2d_delta_grad.cuh", "ss2d_delta_launch.cuh", "ss2d_delta_launch.h"]
+           "ss2d_delta_chain.cuh", "ss2d_delta_split.cuh", "ss2d_delta_grad.cuh", "ss2d_delta_launch.cuh", "ss2d_delta_launch.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

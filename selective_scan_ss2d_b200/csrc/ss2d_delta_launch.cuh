@@ -5,6 +5,7 @@
 #include "ss2d_delta_chain.cuh"
 #include "ss2d_delta_grad.cuh"
 #include "ss2d_delta_launch.h"
+#include "ss2d_delta_split.cuh"
 
 namespace ss2d {
 
@@ -27,6 +28,9 @@ cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
     return cudaGetLastError();
 }
 
+// CTAs of 64 columns of DV above which a chain counts as many (two to an SM)
+constexpr long long kWideCtas = 2 * 148;
+
 // chains of a pass: segments (every slot that may hold one), or sequences
 inline long long delta_units(const DeltaParams &p)
 {
@@ -35,90 +39,115 @@ inline long long delta_units(const DeltaParams &p)
     return p.cu ? p.nslots / p.SC + p.nseq : (long long)p.nseq * ((p.NC + p.SC - 1) / p.SC);
 }
 
-template <typename Tin, int DKP, int NW, int NP, int NPP, int STAGES>
-cudaError_t launch_out(const DeltaParams &p, cudaStream_t st)
+inline dim3 chain_grid(const DeltaParams &p, int tiles)
 {
-    constexpr int smem = ChainLayout<Tin, DKP, NW, kChainOut, NP, NPP, STAGES>::bytes;
-    auto kern = delta_out_kernel<Tin, DKP, NW, NP, NPP, STAGES>;
+    const long long units = delta_units(p);
+    return dim3(tiles, p.H, (unsigned)(units < 65535 ? units : 65535));
+}
+
+// ---- one warp to 16 columns of DV, CTAs of 64 columns
+template <typename Tin, int DKP, int NP, int NPP, int STAGES>
+cudaError_t launch_wide_out(const DeltaParams &p, cudaStream_t st)
+{
+    constexpr int smem = ChainLayout<Tin, DKP, 4, kChainOut, NP, NPP, STAGES>::bytes;
+    auto kern = delta_out_kernel<Tin, DKP, 4, NP, NPP, STAGES>;
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
-    const long long units = delta_units(p);
-    const dim3 grid((p.DV + NW * 16 - 1) / (NW * 16), p.H, (unsigned)(units < 65535 ? units : 65535));
-    kern<<<grid, NW * 32, smem, st>>>(p, units);
+    kern<<<chain_grid(p, (p.DV + 63) / 64), 128, smem, st>>>(p, delta_units(p));
     return cudaGetLastError();
-}
-template <typename Tin, int DKP, int NW, int STAGES>
-cudaError_t launch_both(const DeltaParams &p, cudaStream_t st)
-{
-    constexpr int smem = ChainLayout<Tin, DKP, NW, kChainRev, 3, 3, STAGES>::bytes;
-    auto kern = delta_both_kernel<Tin, DKP, NW, STAGES>;
-    const cudaError_t e = delta_smem(kern, smem);
-    if (e != cudaSuccess)
-        return e;
-    const long long units = delta_units(p);
-    const dim3 grid(2 * ((p.DV + NW * 16 - 1) / (NW * 16)), p.H, (unsigned)(units < 65535 ? units : 65535));
-    kern<<<grid, NW * 32, smem, st>>>(p, units);
-    return cudaGetLastError();
-}
-
-// Stages that fit: a second one hides the next chunk's copies behind this chunk's
-// products; one leaves room for a second and third CTA, which hide them too.
-constexpr int chain_stages(int two_bytes) { return two_bytes <= 225 * 1024 ? 2 : 1; }
-
-// CTAs of four warps (64 columns of DV).  With more of them than two per SM, a
-// single stage and up to three CTAs per SM; otherwise two stages if they fit.
-template <typename Tin, int DKP, int NP, int NPP>
-cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
-{
-    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p);
-    constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainOut, NP, NPP, 2>::bytes);
-    if (two == 1 || ctas > 2 * 148)
-        return launch_out<Tin, DKP, 4, NP, NPP, 1>(p, st);
-    return launch_out<Tin, DKP, 4, NP, NPP, two>(p, st);
 }
 template <typename Tin, int DKP, int MODE>
-cudaError_t launch_one(const DeltaParams &p, cudaStream_t st)
+cudaError_t launch_wide_one(const DeltaParams &p, cudaStream_t st)
 {
     constexpr int smem = ChainLayout<Tin, DKP, 4, MODE, 3, 3, 1>::bytes;
     auto kern = delta_one_kernel<Tin, DKP, 4, 1, MODE>;
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
-    const long long units = delta_units(p);
-    kern<<<dim3((p.DV + 63) / 64, p.H, (unsigned)(units < 65535 ? units : 65535)), 128, smem, st>>>(p, units);
+    kern<<<chain_grid(p, (p.DV + 63) / 64), 128, smem, st>>>(p, delta_units(p));
     return cudaGetLastError();
 }
-// Both chains of a backward pass in one launch while they do not fill the SMs
-// twice; beyond that one after the other: CTAs of both on an SM wait for
-// instructions (6144 chunks of 64 x 64 heads: 3 of 10 cycles a warp waited).
 template <typename Tin, int DKP>
-cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
+cudaError_t launch_wide_both(const DeltaParams &p, cudaStream_t st)
 {
-    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p) * 2;
-    if (ctas > 2 * 148) {
-        const cudaError_t e = launch_one<Tin, DKP, kChainState>(p, st);
-        return e != cudaSuccess ? e : launch_one<Tin, DKP, kChainRev>(p, st);
-    }
-    constexpr int two = chain_stages(ChainLayout<Tin, DKP, 4, kChainRev, 3, 3, 2>::bytes);
-    return launch_both<Tin, DKP, 4, two>(p, st);
+    constexpr int smem = ChainLayout<Tin, DKP, 4, kChainRev, 3, 3, 2>::bytes;
+    auto kern = delta_both_kernel<Tin, DKP, 4, 2>;
+    const cudaError_t e = delta_smem(kern, smem);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<chain_grid(p, 2 * ((p.DV + 63) / 64)), 128, smem, st>>>(p, delta_units(p));
+    return cudaGetLastError();
 }
+
+// ---- four warps to 16 columns: four groups to a CTA and two buffers of K where they fit
+template <typename Tin, int DKP, int MODE, int NP, int NPP>
+struct SplitShape {
+    static constexpr int most = 226 * 1024;
+    static constexpr int groups = SplitLayout<Tin, DKP, 4, MODE, NP, NPP, 2>::bytes <= most ? 4 : 2;
+    static constexpr int kbuf = SplitLayout<Tin, DKP, groups, MODE, NP, NPP, 2>::bytes <= most ? 2 : 1;
+    static constexpr int bytes = SplitLayout<Tin, DKP, groups, MODE, NP, NPP, kbuf>::bytes;
+    static_assert(bytes <= most, "shared memory");
+    static int tiles(int n) { return (n + groups * 16 - 1) / (groups * 16); }
+};
+template <typename Tin, int DKP, int NP, int NPP>
+cudaError_t launch_split_out(const DeltaParams &p, cudaStream_t st)
+{
+    using Sh = SplitShape<Tin, DKP, kChainOut, NP, NPP>;
+    auto kern = delta_split_out_kernel<Tin, DKP, Sh::groups, NP, NPP, Sh::kbuf>;
+    const cudaError_t e = delta_smem(kern, Sh::bytes);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<chain_grid(p, Sh::tiles(p.DV)), Sh::groups * 128, Sh::bytes, st>>>(p, delta_units(p));
+    return cudaGetLastError();
+}
+template <typename Tin, int DKP>
+cudaError_t launch_split_both(const DeltaParams &p, cudaStream_t st)
+{
+    using Sh = SplitShape<Tin, DKP, kChainRev, 3, 3>;   // the larger of the two
+    auto kern = delta_split_both_kernel<Tin, DKP, Sh::groups, Sh::kbuf>;
+    const cudaError_t e = delta_smem(kern, Sh::bytes);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<chain_grid(p, 2 * Sh::tiles(p.DV)), Sh::groups * 128, Sh::bytes, st>>>(p, delta_units(p));
+    return cudaGetLastError();
+}
+
+// Which form a chain takes.  Many chains (more than kWideCtas CTAs): one warp to 16
+// columns, one stage, two or three CTAs per SM.  Few: one warp with two stages for
+// heads of up to 64 in 16 bits (4.4 us a chunk against 5.1 with four warps), four warps for
+// wider heads and float32 (both chains of 4096 tokens, 128 x 128: 533 us against 621; seven
+// float32 sequences of 32 x 64: 67 against 100).
+template <typename Tin, int DKP>
+constexpr bool chain_split() { return sizeof(Tin) == 4 || DKP == 128; }
 
 // the segments' ends and the states that they start from (REV: and end with in reverse)
 template <typename Tin, int DKP, int NP, bool REV>
 cudaError_t launch_segments(const DeltaParams &p, cudaStream_t st)
 {
     constexpr int MODE = REV ? kChainRev : kChainState;   // the larger layout of the pass
-    constexpr int stages = chain_stages(2 * ChainLayout<Tin, DKP, 4, MODE, NP, 3, 2>::bytes);
-    constexpr int smem = ChainLayout<Tin, DKP, 4, MODE, NP, 3, stages>::bytes;
-    auto kern = delta_local_kernel<Tin, DKP, NP, stages, REV>;
-    cudaError_t e = delta_smem(kern, smem);
-    if (e != cudaSuccess)
-        return e;
-    const int dvt = (p.DV + 63) / 64, dkt = (p.DK + 63) / 64;
-    const long long units = delta_units(p);
-    kern<<<dim3(dvt * (REV ? 2 : 1) + dkt, p.H, (unsigned)(units < 65535 ? units : 65535)), 128, smem, st>>>(p, dvt, dkt,
-                                                                                                          units);
+    cudaError_t e;
+    if constexpr (chain_split<Tin, DKP>()) {
+        using Sh = SplitShape<Tin, DKP, MODE, NP, 3>;
+        auto kern = delta_split_local_kernel<Tin, DKP, Sh::groups, NP, Sh::kbuf, REV>;
+        e = delta_smem(kern, Sh::bytes);
+        if (e != cudaSuccess)
+            return e;
+        const int dvt = Sh::tiles(p.DV), dkt = Sh::tiles(p.DK);
+        kern<<<chain_grid(p, dvt * (REV ? 2 : 1) + dkt), Sh::groups * 128, Sh::bytes, st>>>(p, dvt, dkt,
+                                                                                           delta_units(p));
+    } else {
+        // two stages where two such CTAs fit an SM
+        constexpr int two = ChainLayout<Tin, DKP, 4, MODE, NP, 3, 2>::bytes;
+        constexpr int stages = 2 * two <= 225 * 1024 ? 2 : 1;
+        constexpr int smem = ChainLayout<Tin, DKP, 4, MODE, NP, 3, stages>::bytes;
+        auto kern = delta_local_kernel<Tin, DKP, NP, stages, REV>;
+        e = delta_smem(kern, smem);
+        if (e != cudaSuccess)
+            return e;
+        const int dvt = (p.DV + 63) / 64, dkt = (p.DK + 63) / 64;
+        kern<<<chain_grid(p, dvt * (REV ? 2 : 1) + dkt), 128, smem, st>>>(p, dvt, dkt, delta_units(p));
+    }
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -129,6 +158,34 @@ cudaError_t launch_segments(const DeltaParams &p, cudaStream_t st)
         return e;
     comb<<<dim3(p.DV / 16 * (REV ? 2 : 1), p.H, p.nseq < 65535 ? p.nseq : 65535), CL::threads, CL::bytes, st>>>(p);
     return cudaGetLastError();
+}
+
+template <typename Tin, int DKP, int NP, int NPP>
+cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
+{
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p);
+    if (ctas > kWideCtas)
+        return launch_wide_out<Tin, DKP, NP, NPP, 1>(p, st);
+    if constexpr (chain_split<Tin, DKP>())
+        return launch_split_out<Tin, DKP, NP, NPP>(p, st);
+    else
+        return launch_wide_out<Tin, DKP, NP, NPP, 2>(p, st);
+}
+// Both chains of a backward pass in one launch while they do not fill the SMs
+// twice; beyond that one after the other: CTAs of both on an SM wait for
+// instructions (6144 chunks of 64 x 64 heads: 3 of 10 cycles a warp waited).
+template <typename Tin, int DKP>
+cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
+{
+    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p);
+    if (ctas * 2 > kWideCtas) {
+        const cudaError_t e = launch_wide_one<Tin, DKP, kChainState>(p, st);
+        return e != cudaSuccess ? e : launch_wide_one<Tin, DKP, kChainRev>(p, st);
+    }
+    if constexpr (chain_split<Tin, DKP>())
+        return launch_split_both<Tin, DKP>(p, st);
+    else
+        return launch_wide_both<Tin, DKP>(p, st);
 }
 
 template <typename Tin, int DKP, bool SHARED>
