@@ -409,14 +409,16 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * NULL = not wanted; h_last may be h0, otherwise no output may overlap an input.  A
  * sequence of no tokens gets h_last = h0.
  * All pointers DEVICE pointers of the current device (SS2D_ERR_PTR otherwise),
- * 16-byte aligned.  Asynchronous on `stream`; scratch (per 64 tokens and head 24 to
- * 50 KB) comes from the stream-ordered pool.
+ * 16-byte aligned.  Asynchronous on `stream`; scratch (per 64 tokens and head 21 to
+ * 31 KB, for float16 and float32 also 512 or 768 DKP bytes per key head, DKP = 64 or
+ * 128, DK rounded up; for few long sequences three states per head and segment) comes
+ * from the stream-ordered pool.  L < 2^31 - 64.
  *
  * Precision: the state and all arithmetic are float32 (products on the tensor
  * cores of operands split into bfloat16 parts that hold them to float32 accuracy);
  * o is rounded once, on store.  Where o is 16 bits and no h_last is asked for,
  * intermediate values keep 16 bits of mantissa.  A value that is not finite
- * reaches every output of its sequence from its group of 64 tokens on. */
+ * may reach every output of its sequence from its group of 64 tokens on. */
 int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const float *g,
                          const float *beta, const float *h0, void *o, float *h_last,
                          const int *cu_seqlens, int nseq, int L, int HK, int H, int DK, int DV,
@@ -430,8 +432,8 @@ int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const floa
  * a fixed order; dg, dbeta (tokens, H) float32; dh0 (nseq, H, DK, DV) float32 or NULL
  * (not wanted; may be dh_last).  The forward's other arguments and rules hold.
  * The states are computed again from the inputs and kept in scratch: per 64 tokens
- * and head 8 * DKP * DV + 784 * DV + 49920 bytes (DKP = 64 or 128, DK rounded up), from
- * the stream-ordered pool.  No atomics: the same bits on every call. */
+ * and head 8 * DKP * DV + 512 * DV + 31488 bytes besides the forward's, from the
+ * stream-ordered pool.  No atomics: the same bits on every call. */
 int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const float *g,
                          const float *beta, const float *h0, const void *dout,
                          const float *dh_last, void *dq, void *dk, void *dv, float *dg,

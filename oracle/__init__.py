@@ -22,7 +22,10 @@ forward definition, pinned against finite differences of the C forward;
 ``ss2d_front_np.py`` writes out the front that feeds the scan in the
 tutorial's SelectiveSSM (causal depthwise conv1d, SiLU, x_proj, dt_proj) and
 its per-direction form of the Vim block; :func:`front_scan` runs it and then
-the scan of every direction, pinned in ``tests/test_oracle_front.py``.  Every part is pinned by ``tests/test_oracle_pins.py``
+the scan of every direction, pinned in ``tests/test_oracle_front.py``.
+``gated_delta_np.py`` and ``block_norm_np.py`` write out the gated delta rule
+and the block norms with their gradients, pinned in
+``tests/test_gated_delta.py`` and ``tests/test_block_norm.py``.  Every part is pinned by ``tests/test_oracle_pins.py``
 against closed forms, a matrix-exponential discretisation, an O(L^2) brute
 force and exact index-map invariants; parity is pinned for every function
 (no function here is "parity unpinned").

@@ -1,7 +1,9 @@
 """B200-native (sm_100a) SS2D path: cross_scan -> selective scan ->
 cross_merge, and the 1D one- or two-direction selective scan of Vision Mamba;
 forward (plain, gated by SiLU(z), or returning the final states) and backward
-(every input's gradient).
+(every input's gradient).  Beside them the gated delta rule (whole or packed
+sequences, its gradients, one token with the states in place) and the block
+norms (a mixer's output norm and gate, the scaled residual, the next norm).
 
 The computation lives in the CUDA library built from ``csrc/`` (C ABI in
 ``include/ss2d.h``); :mod:`.binding` marshals torch tensors into it.

@@ -33,7 +33,7 @@ size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 int validate(const Call &c)
 {
     const DeltaParams &p = c.p;
-    if (p.nseq < 0 || p.L < 0 || p.HK < 0 || p.H < 0 || p.H > 65535)
+    if (p.nseq < 0 || p.L < 0 || p.L > INT_MAX - kDeltaC || p.HK < 0 || p.H < 0 || p.H > 65535)
         return SS2D_ERR_SHAPE;
     if (c.dtype != SS2D_F32 && c.dtype != SS2D_BF16 && c.dtype != SS2D_F16)
         return SS2D_ERR_DTYPE;

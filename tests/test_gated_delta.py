@@ -125,6 +125,8 @@ def test_argument_errors_are_reported_without_cuda(lib, call):
     keep, p = ptr()
     assert call(lib, p, nseq=-1) == -2
     assert call(lib, p, L=-1) == -2
+    if call is not _step:
+        assert call(lib, p, L=2 ** 31 - 1) == -2
     assert call(lib, p, HK=1, H=70000, vs=70000 * 16) == -2
     assert call(lib, p, dtype=5) == -3
     assert call(lib, p, HK=2, H=3, qs=32, ks=32, vs=48) == -14
