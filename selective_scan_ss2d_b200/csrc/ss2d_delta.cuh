@@ -572,8 +572,9 @@ constexpr int kPrepThreads = 128;
 
 template <int DKP, int NPI, int NPT, int NPP>
 struct PrepLayout {
-    static constexpr int oX = NPT * kTriBytes;                 // P, then T; A before it
-    static constexpr int oD = oX + (NPT > NPP ? NPT : NPP) * kTriBytes;
+    static constexpr int oT = NPT * kTriBytes;                 // T; A before it
+    static constexpr int oP = oT + NPT * kTriBytes;            // a block of P for each warp
+    static constexpr int oD = oP + 4 * NPP * 512;
     static constexpr int head = oD + 4 * 16 * 20 * 4;          // diagonal blocks of A, rows of 20 floats
     static constexpr int tiles = 2 * NPI * kDeltaC * DKP * 2;  // K and Q, read before the heads
     static constexpr int bytes = tiles > head ? tiles : head;
@@ -747,13 +748,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
             delta_rows_product<DKP, NPI, 2>(smem_addr(qt), smem_addr(kt), bi(n) * 16, bj(n) * 16, qk[n]);
         }
     }
-    const uint32_t sA = smem_addr(dsm), sX = sA + Lay::oX;
+    const uint32_t sA = smem_addr(dsm), sX = sA + Lay::oT;
+    unsigned char *pw = dsm + Lay::oP + warp * NPP * 512;   // the warp's block of P
     float *dg = reinterpret_cast<float *>(dsm + Lay::oD);   // [4][16][20]
     const int nb = (min(q.len - t0, kDeltaC) + 15) / 16;    // 16-token blocks that hold tokens
-    // a head's P or T from shared memory to scratch
-    auto leave = [&](void *dst, int bytes) {
-        for (int i = tid; i < bytes / 16; i += kPrepThreads)
-            reinterpret_cast<uint4 *>(dst)[i] = *reinterpret_cast<const uint4 *>(dsm + Lay::oX + i * 16);
+    // a block of N parts, `from` bytes apart, to the block's place in a head's scratch, by one warp
+    auto leave = [&](void *dst, long long sh, int N, int I, int J, const unsigned char *src, int from) {
+        char *d = static_cast<char *>(dst) + sh * N * kTriBytes + tri_block(I, J) + lane * 16;
+        for (int m = 0; m < N; ++m)
+            *reinterpret_cast<uint4 *>(d + m * kTriBytes) = *reinterpret_cast<const uint4 *>(src + m * from + lane * 16);
     };
     for (int hi = 0; hi < G; ++hi) {
         const int h = hk * G + hi;
@@ -789,12 +792,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
                     const float k0 = kk[n][t][hf * 2], k1 = kk[n][t][hf * 2 + 1];
                     const float q0 = qk[n][t][hf * 2], q1 = qk[n][t][hf * 2 + 1];
                     const bool on0 = !diag || j <= i, on1 = !diag || j < i;
-                    const uint32_t o = tri_block(I, J) + tri_piece(i, t) + (lane & 3) * 4;
+                    const uint32_t in = tri_piece(i, t) + (lane & 3) * 4, o = tri_block(I, J) + in;
                     uint32_t w[NPP], u[NPT];
                     split2<NPP>(on0 ? p.scale * D0 * q0 : 0.f, on1 ? p.scale * D1 * q1 : 0.f, w);
 #pragma unroll
                     for (int m = 0; m < NPP; ++m)
-                        *reinterpret_cast<uint32_t *>(dsm + Lay::oX + m * kTriBytes + o) = w[m];
+                        *reinterpret_cast<uint32_t *>(pw + m * 512 + in) = w[m];
                     if (!diag) {
                         split2<NPT>(bi_ * D0 * k0, bi_ * D1 * k1, u);
 #pragma unroll
@@ -806,9 +809,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
                     }
                 }
             }
+            __syncwarp();
+            leave(p.Pp, sh, NPP, I, J, pw, 512);
+            __syncwarp();
         }
-        __syncthreads();
-        leave(static_cast<char *>(p.Pp) + sh * NPP * kTriBytes, NPP * kTriBytes);
+        __syncthreads();   // A and its diagonal blocks are here
         // column j = lane of the diagonal block's inverse
         float col[16];
         if (lane < 16) {
@@ -830,12 +835,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
                 col[i] = (i == lane ? 1.f : 0.f) - (a0 + a1);   // zero above the diagonal by itself
             }
         }
-        __syncthreads();   // P has left
         if (lane < 16) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float x = col[i];
-                unsigned char *o = dsm + Lay::oX + tri_block(warp, warp) + tri_piece(i, lane >> 3) + (lane & 7) * 2;
+                unsigned char *o = dsm + Lay::oT + tri_block(warp, warp) + tri_piece(i, lane >> 3) + (lane & 7) * 2;
 #pragma unroll
                 for (int m = 0; m < NPT; ++m) {
                     const __nv_bfloat16 b = __float2bfloat16_rn(x);
@@ -873,8 +877,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
             }
             __syncwarp();
         }
-        __syncthreads();
-        leave(static_cast<char *>(p.Tp) + sh * NPT * kTriBytes, NPT * kTriBytes);
+        for (int i = warp; i < 4; ++i)
+            leave(p.Tp, sh, NPT, i, warp, dsm + Lay::oT + tri_block(i, warp), kTriBytes);
     }
 }
 
