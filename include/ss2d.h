@@ -500,7 +500,7 @@ int block_norm_fwd(const void *x, const void *z, const void *r, const float *s,
  * dw_pre, db_pre (D): each in a fixed order, the same bits on every call.
  * With no rows the sums are zero.  dr may be dr_out, and dx may be x if x is
  * contiguous; otherwise no output may overlap an input or another output.
- * Scratch for the partial sums (5920 * D bytes at most) comes from the
+ * Scratch for the partial sums (8880 * D bytes at most) comes from the
  * stream-ordered pool. */
 int block_norm_bwd(const void *x, const void *z, const void *r_out, const float *s,
                    const float *w_post, const float *b_post, const float *w_pre,

@@ -97,9 +97,9 @@ ss2d::NormPlan norm_plan(NormCall &c, bool bwd)
         const bool known = has == kHasPost || has == (kHasPost | kHasGate) || has == (kHasRes | kHasPre) ||
                            has == (kHasRes | kHasPre | kHasScale | kHasBias) ||
                            has == (kHasPost | kHasGate | kHasRes | kHasPre | kHasScale);
-        if (known && team(8) * 8 == p.D) {
+        if (known && team(8) * 8 == p.D && team(8) <= 256) {
             pl.M = has;
-        } else if (known && team(12) * 12 == p.D) {
+        } else if (known && team(12) * 12 == p.D && team(12) <= 256) {
             pl = NormPlan{4, 12, has};
         }
     }
@@ -234,8 +234,9 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
     const ss2d::NormPlan pl = norm_plan(c, true);
     const int threads = p.tpr > 256 ? p.tpr : 256;
     const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
-    // two CTAs of 256 threads at the kernel's registers fill an SM; more CTAs only add partials
-    const int grid = ctas > 148 * 2 ? 148 * 2 : (int)ctas;
+    // CTAs that the kernel's registers let onto an SM; more of them only add partials
+    const int fill = 148 * (pl.M == ss2d::kNormAny ? 2 : ss2d::norm_bwd_ctas(pl.E));
+    const int grid = ctas > fill ? fill : (int)ctas;
     void *part = nullptr;
     if (p.cols) {
         rc = ss2d::scratch_alloc(&part, sizeof(float) * ss2d::kNormCols * grid * (size_t)D, st);

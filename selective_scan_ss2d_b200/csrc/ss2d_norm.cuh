@@ -158,14 +158,21 @@ __device__ __forceinline__ void norm_store(T *row, int col, const float *v)
         for (int i = 0; i < V; i += 4)
             *reinterpret_cast<float4 *>(row + col + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     } else {
-        __align__(16) T h[V];
+        uint32_t h[V / 2];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            h[i] = norm_round<T>(v[i]);
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const __half2 t = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                h[i] = *reinterpret_cast<const uint32_t *>(&t);
+            } else {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                h[i] = *reinterpret_cast<const uint32_t *>(&t);
+            }
+        }
         if constexpr (V == 8)
-            *reinterpret_cast<uint4 *>(row + col) = *reinterpret_cast<const uint4 *>(h);
+            *reinterpret_cast<uint4 *>(row + col) = make_uint4(h[0], h[1], h[2], h[3]);
         else
-            *reinterpret_cast<uint2 *>(row + col) = *reinterpret_cast<const uint2 *>(h);
+            *reinterpret_cast<uint2 *>(row + col) = make_uint2(h[0], h[1]);
     }
 }
 
@@ -182,7 +189,18 @@ __device__ __forceinline__ long long norm_row(long long i, int group, long long 
 
 // 1 / (1 + e^-z) on the multi-function unit: e^-z off by 2^-22 + 2^-23 |z|, the reciprocal by 2^-23 (relative);
 // e^-z = inf gives 0
-__device__ __forceinline__ float norm_sigmoid(float z) { return __fdividef(1.f, 1.f + mufu_ex2(-z * kLog2e)); }
+__device__ __forceinline__ float norm_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 norm_sigmoid2(float2 z)
+{
+    const float2 t = __fmul2_rn(z, make_float2(-kLog2e, -kLog2e));
+    const float2 e = __fadd2_rn(make_float2(mufu_ex2(t.x), mufu_ex2(t.y)), make_float2(1.f, 1.f));
+    return make_float2(norm_rcp(e.x), norm_rcp(e.y));
+}
 
 // Sums over a team.  Teams up to a warp: butterfly shuffles inside the team
 // (every lane ends with the same bits).  Larger teams: one value per warp
@@ -203,19 +221,28 @@ struct TeamSum {
     // both sums at once
     __device__ __forceinline__ float2 operator()(float a, float b)
     {
-        for (int o = (tpr < 32 ? tpr : 32) >> 1; o; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
+        if (tpr >= 32) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                b += __shfl_xor_sync(0xffffffffu, b, o);
+            }
+        } else {
+            for (int o = tpr >> 1; o; o >>= 1) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                b += __shfl_xor_sync(0xffffffffu, b, o);
+            }
         }
         if (nw > 1) {   // uniform over the CTA
+            float2 *r = red + buf * 32;
             if ((threadIdx.x & 31) == 0)
-                red[buf * 32 + warp] = make_float2(a, b);
+                r[warp] = make_float2(a, b);
             __syncthreads();
             a = b = 0.f;
-            for (int i = 0; i < nw; ++i) {
-                const float2 v = red[buf * 32 + w0 + i];
-                a += v.x;
-                b += v.y;
+            for (int i = 0; i < nw; i += 2) {   // two warps' sums to a read
+                const float4 v = *reinterpret_cast<const float4 *>(r + w0 + i);
+                a += v.x + v.z;
+                b += v.y + v.w;
             }
             buf ^= 1;
         }
@@ -223,45 +250,85 @@ struct TeamSum {
     }
     __device__ __forceinline__ float operator()(float a)
     {
-        for (int o = (tpr < 32 ? tpr : 32) >> 1; o; o >>= 1)
-            a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (tpr >= 32) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+        } else {
+            for (int o = tpr >> 1; o; o >>= 1)
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+        }
         if (nw > 1) {
+            float *r = reinterpret_cast<float *>(red + buf * 32);
             if ((threadIdx.x & 31) == 0)
-                red[buf * 32 + warp].x = a;
+                r[warp] = a;
             __syncthreads();
             a = 0.f;
-            for (int i = 0; i < nw; ++i)
-                a += red[buf * 32 + w0 + i].x;
+            for (int i = 0; i < nw; i += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(r + w0 + i);
+                a += v.x + v.y;
+            }
             buf ^= 1;
         }
         return a;
     }
 };
 
-// v <- normalised v (values past the row's end stay zero); returns 1 / sqrt(. + eps)
+// Pairs of a thread's values, on the packed float32 instructions (each lane
+// rounds as the single one does): the kernels are bound by instructions before bytes.
+__device__ __forceinline__ float2 pair(const float *v, int k) { return make_float2(v[2 * k], v[2 * k + 1]); }
+__device__ __forceinline__ void set_pair(float *v, int k, float2 x)
+{
+    v[2 * k] = x.x;
+    v[2 * k + 1] = x.y;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+template <int E>
+__device__ __forceinline__ float norm_total(const float (&v)[E])
+{
+    float2 a = pair(v, 0);
+#pragma unroll
+    for (int k = 1; k < E / 2; ++k)
+        a = __fadd2_rn(a, pair(v, k));
+    return a.x + a.y;
+}
+template <int E>
+__device__ __forceinline__ float norm_dot(const float (&v)[E], const float (&w)[E])
+{
+    float2 a = __fmul2_rn(pair(v, 0), pair(w, 0));
+#pragma unroll
+    for (int k = 1; k < E / 2; ++k)
+        a = __ffma2_rn(pair(v, k), pair(w, k), a);
+    return a.x + a.y;
+}
+// v <- v - m, values past the row's end stay zero
 template <int E, typename In>
-__device__ __forceinline__ float norm_rows(float (&v)[E], int how, int D, float eps, TeamSum &sum, In in)
+__device__ __forceinline__ void norm_shift(float (&v)[E], float m, In in)
+{
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+        const float2 d = __fadd2_rn(pair(v, k), both(-m));
+        v[2 * k] = in(2 * k) ? d.x : 0.f;
+        v[2 * k + 1] = in(2 * k + 1) ? d.y : 0.f;
+    }
+}
+template <int E>
+__device__ __forceinline__ void norm_times(float (&v)[E], float f)
+{
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k)
+        set_pair(v, k, __fmul2_rn(pair(v, k), both(f)));
+}
+
+// v <- normalised v (values past the row's end stay zero)
+template <int E, typename In>
+__device__ __forceinline__ void norm_rows(float (&v)[E], int how, int D, float eps, TeamSum &sum, In in)
 {
     const float invD = 1.f / (float)D;
-    if (how == kNormLayer) {
-        float a = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            a += v[e];
-        const float m = sum(a) * invD;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            v[e] = in(e) ? v[e] - m : 0.f;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        q = fmaf(v[e], v[e], q);
-    const float rs = 1.f / sqrtf(sum(q) * invD + eps);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        v[e] *= rs;
-    return rs;
+    if (how == kNormLayer)
+        norm_shift<E>(v, sum(norm_total<E>(v)) * invD, in);
+    norm_times<E>(v, rsqrtf(sum(norm_dot<E>(v, v)) * invD + eps));
 }
 // mean and 1 / sqrt(. + eps) of two rows at once (how none: 0 and 1), each as norm_rows has them
 template <int E, typename GetA, typename GetB, typename In>
@@ -271,79 +338,67 @@ __device__ __forceinline__ void norm_stats2(GetA getA, int howA, GetB getB, int 
     const float invD = 1.f / (float)D;
     mean = make_float2(0.f, 0.f);
     rs = make_float2(1.f, 1.f);
-    float v[E];
+    if (howA == kNormNone && howB == kNormNone)
+        return;
+    float v[E], a = 0.f, b = 0.f;
     if (howA == kNormLayer || howB == kNormLayer) {
-        float a = 0.f, b = 0.f;
         if (howA == kNormLayer) {
             getA(v);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                a += v[e];
+            a = norm_total<E>(v);
         }
         if (howB == kNormLayer) {
             getB(v);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                b += v[e];
+            b = norm_total<E>(v);
         }
         mean = sum(a, b);
         mean.x *= invD;
         mean.y *= invD;
+        a = b = 0.f;
     }
-    if (howA == kNormNone && howB == kNormNone)
-        return;
-    float a = 0.f, b = 0.f;
     if (howA != kNormNone) {
         getA(v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = in(e) ? v[e] - mean.x : 0.f;
-            a = fmaf(d, d, a);
-        }
+        if (howA == kNormLayer)
+            norm_shift<E>(v, mean.x, in);
+        a = norm_dot<E>(v, v);
     }
     if (howB != kNormNone) {
         getB(v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = in(e) ? v[e] - mean.y : 0.f;
-            b = fmaf(d, d, b);
-        }
+        if (howB == kNormLayer)
+            norm_shift<E>(v, mean.y, in);
+        b = norm_dot<E>(v, v);
     }
     const float2 q = sum(a, b);
     if (howA != kNormNone)
-        rs.x = 1.f / sqrtf(q.x * invD + eps);
+        rs.x = rsqrtf(q.x * invD + eps);
     if (howB != kNormNone)
-        rs.y = 1.f / sqrtf(q.y * invD + eps);
+        rs.y = rsqrtf(q.y * invD + eps);
 }
 // d <- rs (d - n mean(d n) - [layer] mean(d))
 template <int E, typename In>
 __device__ __forceinline__ void norm_grad(float (&d)[E], const float (&n)[E], float rs, int how, int D,
                                           TeamSum &sum, In in)
 {
-    const float invD = 1.f / (float)D;
-    float a = 0.f, b = 0.f;
+    const float f = rs / (float)D, a = norm_dot<E>(d, n);
+    float2 m = make_float2(0.f, 0.f);
+    if (how == kNormLayer)
+        m = sum(a, norm_total<E>(d));
+    else
+        m.x = sum(a);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        a = fmaf(d[e], n[e], a);
-        b += d[e];
+    for (int k = 0; k < E / 2; ++k) {
+        float2 t = __ffma2_rn(pair(n, k), both(-m.x * f), __fmul2_rn(pair(d, k), both(rs)));
+        if (how == kNormLayer)
+            t = __fadd2_rn(t, both(-m.y * f));
+        d[2 * k] = in(2 * k) ? t.x : 0.f;
+        d[2 * k + 1] = in(2 * k + 1) ? t.y : 0.f;
     }
-    float ma, mb = 0.f;
-    if (how == kNormLayer) {
-        const float2 m = sum(a, b);
-        ma = m.x * invD;
-        mb = m.y * invD;
-    } else {
-        ma = sum(a) * invD;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        d[e] = in(e) ? rs * (d[e] - n[e] * ma - mb) : 0.f;
 }
 
 // What a call has, as kernels are compiled for: the parts below, for rows that fill
 // their teams (D = TPR * E), or kNormAny: whatever the parameters say.  With every part
 // looked up and every column compared in the loop, the gated norm of 302592 rows of 64
-// values issued 35 instructions a value and took 29 us, at 72 % of the issue slots.
+// values issued 35 instructions a value and took 29 us, at 72 % of the issue slots; with
+// the combination compiled and packed arithmetic 22 us.
 enum { kHasPost = 1, kHasGate = 2, kHasRes = 4, kHasPre = 8, kHasScale = 16, kHasBias = 32, kNormAny = -1 };
 
 // grid: CTAs of blockDim.x / tpr teams, one row per team and step; the next
@@ -352,7 +407,7 @@ enum { kHasPost = 1, kHasGate = 2, kHasRes = 4, kHasPre = 8, kHasScale = 16, kHa
 template <typename Tin, typename Tr, int V, int E, int M>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
 {
-    __shared__ float2 red[64];
+    __shared__ __align__(16) float2 red[64];
     constexpr bool any = M == kNormAny;
     const bool post = any ? p.post != kNormNone : M & kHasPost, gate = any ? p.z != nullptr : M & kHasGate,
                res = any ? p.r != nullptr : M & kHasRes, pre = any ? p.pre != kNormNone : M & kHasPre,
@@ -389,8 +444,8 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
     auto times = [&](float *v, int i, const float *src, const float (&w)[K]) {
         if constexpr (!any) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[j] *= w[i * V + j];
+            for (int k = 0; k < V / 2; ++k)
+                set_pair(v, k, __fmul2_rn(pair(v, k), pair(w + i * V, k)));
         } else if (src) {
             float t[V];
             norm_load<float, V>(src, col(i), t);
@@ -448,8 +503,8 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
             zr.get(w);
             load_z(o + step);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                v[e] *= w[e] * norm_sigmoid(w[e]);
+            for (int k = 0; k < E / 2; ++k)
+                set_pair(v, k, __fmul2_rn(pair(v, k), __fmul2_rn(pair(w, k), norm_sigmoid2(pair(w, k)))));
         }
         if (scale) {
 #pragma unroll
@@ -461,8 +516,8 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
             rr.get(w);
             load_r(o + step);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                v[e] += w[e];
+            for (int k = 0; k < E / 2; ++k)
+                set_pair(v, k, __fadd2_rn(pair(v, k), pair(w, k)));
         }
 #pragma unroll
         for (int i = 0; i < E / V; ++i)
@@ -483,18 +538,23 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
     }
 }
 
+// CTAs of 256 threads per SM of the compiled combinations
+__host__ __device__ constexpr int norm_bwd_ctas(int E) { return E == 8 ? 3 : 2; }
+
 // dynamic shared memory: blockDim.x * E floats (the teams' column sums).  BIAS:
-// the sums for biases are kept too (two of five, 16 registers).  The next row's
-// vectors are on their way while a row's sums go round, and both norms' statistics
-// go round together: with loads where they are used and every sum by itself,
-// 12544 rows of 1024 values with every part took 144 us.
+// the sums for biases are kept too (two of five, 16 registers).  Both norms'
+// statistics go round the team together.  Measured on 12544 rows of 1024 values with every
+// part: loads where they are used and every sum by itself 144 us; the next row ahead 94;
+// compiled combinations 69; packed arithmetic, unrolled sums and three CTAs 65 (2.6 TB/s,
+// 63 % of the issue slots: the rounds of sums, a third of the instructions, bound it).
 template <typename Tin, typename Tr, int V, int E, bool BIAS, int M>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
+__global__ void __launch_bounds__(M == kNormAny ? 512 : 256, M == kNormAny ? 1 : norm_bwd_ctas(E)) norm_bwd_kernel(const NormParams p)
 {
     constexpr int NC = BIAS ? kNormCols : 3;
-    constexpr bool ahead = E < 16;   // rows of 4097 values and more have no registers for it
+    // next row ahead, or a third CTA per SM, which hides as much; rows of 4097 values and more have registers for neither
+    constexpr bool ahead = M == kNormAny ? E < 16 : norm_bwd_ctas(E) == 2;
     extern __shared__ __align__(16) float csum[];
-    __shared__ float2 red[64];
+    __shared__ __align__(16) float2 red[64];
     const int lane = threadIdx.x % p.tpr, team = threadIdx.x / p.tpr, teams = blockDim.x / p.tpr;
     constexpr bool any = M == kNormAny;
     const bool post = any ? p.post != kNormNone : M & kHasPost, gate = any ? p.z != nullptr : M & kHasGate,
@@ -512,13 +572,17 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
 #pragma unroll
         for (int e = 0; e < E; ++e)
             acc[c][e] = 0.f;
-    auto vec = [&](const float *w, int i, float one, float (&o)[V]) {
-        if (w) {
-            norm_load<float, V>(w, col(i), o);
-        } else {
+    // a weight's values of the thread's columns, `one` where it is not there or past the row's end
+    auto weights = [&](const float *w, float one, float (&o)[E]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                o[j] = one;
+        for (int i = 0; i < E / V; ++i) {
+            if (w && on(i)) {
+                norm_load<float, V>(w, col(i), o + i * V);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    o[i * V + j] = one;
+            }
         }
     };
     const long long step = (long long)gridDim.x * teams;
@@ -576,23 +640,21 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
             yr.get(g);
             if constexpr (ahead)
                 row_pre(o + step);
+            if (p.pre == kNormLayer)
+                norm_shift<E>(a, mean.x, in);
+            norm_times<E>(a, rs.x);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                a[e] = in(e) ? (a[e] - mean.x) * rs.x : 0.f;
-#pragma unroll
-            for (int i = 0; i < E / V; ++i) {
-                float w[V];
-                if (on(i))
-                    vec(p.w_pre, i, 1.f, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int e = i * V + j;
-                    acc[2][e] = fmaf(g[e], a[e], acc[2][e]);
-                    if constexpr (BIAS)
-                        acc[4][e] += g[e];
-                    g[e] = on(i) ? g[e] * w[j] : 0.f;
-                }
+            for (int k = 0; k < E / 2; ++k) {
+                const float2 gk = pair(g, k);
+                set_pair(acc[2], k, __ffma2_rn(gk, pair(a, k), pair(acc[2], k)));
+                if constexpr (BIAS)
+                    set_pair(acc[4], k, __fadd2_rn(gk, pair(acc[4], k)));
             }
+            float w[E];
+            weights(p.w_pre, 1.f, w);
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k)
+                set_pair(g, k, __fmul2_rn(pair(g, k), pair(w, k)));
             norm_grad<E>(g, a, rs.x, p.pre, D, sum, in);
         }
         if (p.dr_out) {
@@ -600,8 +662,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
             if constexpr (ahead)
                 row_g(o + step);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                g[e] += a[e];
+            for (int k = 0; k < E / 2; ++k)
+                set_pair(g, k, __fadd2_rn(pair(g, k), pair(a, k)));
         }
         if (p.dr) {
 #pragma unroll
@@ -614,45 +676,65 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p)
         if constexpr (ahead)
             row_x(o + step);
         if (post) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                a[e] = in(e) ? (a[e] - mean.y) * rs.y : 0.f;
+            if (p.post == kNormLayer)
+                norm_shift<E>(a, mean.y, in);
+            norm_times<E>(a, rs.y);
         }
+        {
+            float w[E], z[E];   // w_post, s
+            weights(post ? p.w_post : nullptr, 1.f, w);
+            weights(scale ? p.s : nullptr, 1.f, z);
+            float pv[E];
+            if (post && bias && p.b_post) {
+                weights(p.b_post, 0.f, pv);
 #pragma unroll
-        for (int i = 0; i < E / V; ++i) {
-            float w[V], b[V], s[V], z[V], dz[V];
+                for (int k = 0; k < E / 2; ++k)
+                    set_pair(pv, k, __ffma2_rn(pair(a, k), pair(w, k), pair(pv, k)));
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                w[j] = b[j] = s[j] = z[j] = 0.f;
-            if (on(i)) {
-                vec(post ? p.w_post : nullptr, i, 1.f, w);
-                vec(post && bias ? p.b_post : nullptr, i, 0.f, b);
-                vec(scale ? p.s : nullptr, i, 1.f, s);
+                for (int k = 0; k < E / 2; ++k)
+                    set_pair(pv, k, post ? __fmul2_rn(pair(a, k), pair(w, k)) : pair(a, k));
             }
-            if (gate)
-                zr.v[i].get(z);
+            // g: G, then dt = s G; ds takes G t, t = p SiLU(z)
+            if (gate) {
+                float zz[E];
+                zr.get(zz);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int e = i * V + j;
-                const float pv = fmaf(a[e], w[j], b[j]);
-                float gt = 1.f, dgate = 0.f;
-                if (gate) {
-                    const float sg = norm_sigmoid(z[j]);
-                    gt = z[j] * sg;
-                    dgate = sg * fmaf(z[j], 1.f - sg, 1.f);
+                for (int k = 0; k < E / 2; ++k) {
+                    const float2 zk = pair(zz, k), sg = norm_sigmoid2(zk), gt = __fmul2_rn(zk, sg);
+                    const float2 gk = pair(g, k), pk = pair(pv, k);
+                    if (scale)
+                        set_pair(acc[0], k, __ffma2_rn(gk, __fmul2_rn(pk, gt), pair(acc[0], k)));
+                    const float2 dt = scale ? __fmul2_rn(gk, pair(z, k)) : gk;
+                    // SiLU'(z) = sg (1 + z (1 - sg)) = sg + z sg - (z sg) sg
+                    const float2 dg = __ffma2_rn(gt, __ffma2_rn(sg, both(-1.f), both(1.f)), sg);
+                    set_pair(zz, k, __fmul2_rn(__fmul2_rn(dt, pk), dg));
+                    set_pair(g, k, __fmul2_rn(dt, gt));   // dp
                 }
-                if (scale)
-                    acc[0][e] = fmaf(g[e], pv * gt, acc[0][e]);
-                const float dt = s[j] * g[e];
-                dz[j] = dt * pv * dgate;
-                const float dp = dt * gt;
-                acc[1][e] = fmaf(dp, a[e], acc[1][e]);
-                if constexpr (BIAS)
-                    acc[3][e] += dp;
-                g[e] = dp * w[j];
+                if (p.dz) {
+#pragma unroll
+                    for (int i = 0; i < E / V; ++i)
+                        if (live && on(i))
+                            norm_store<Tin, V>(static_cast<Tin *>(p.dz) + o * D, col(i), zz + i * V);
+                }
+            } else if (scale) {
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k) {
+                    const float2 gk = pair(g, k);
+                    set_pair(acc[0], k, __ffma2_rn(gk, pair(pv, k), pair(acc[0], k)));
+                    set_pair(g, k, __fmul2_rn(gk, pair(z, k)));
+                }
             }
-            if (gate && p.dz && live && on(i))
-                norm_store<Tin, V>(static_cast<Tin *>(p.dz) + o * D, col(i), dz);
+            if (post) {
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k) {
+                    const float2 dp = pair(g, k);
+                    set_pair(acc[1], k, __ffma2_rn(dp, pair(a, k), pair(acc[1], k)));
+                    if constexpr (BIAS)
+                        set_pair(acc[3], k, __fadd2_rn(dp, pair(acc[3], k)));
+                    set_pair(g, k, __fmul2_rn(dp, pair(w, k)));
+                }
+            }
         }
         if constexpr (ahead)
             row_z(o + step);

@@ -7,7 +7,7 @@ the float32 arithmetic.  That is a sum over a row by a tree whose longest
 path is E + log2(TPR) + TPR / 32 <= 16 + 9 + 16 additions and at most 20
 operations on each value, each off by 2^-24 of a quantity no larger than the
 row's largest (M, below): F32 = 64 * 2^-24 * M.  Column sums over rows add
-one value per visited row, then teams (<= 64), partials (<= 296 / 32) and 32
+one value per visited row, then teams (<= 64), partials (<= 444 / 32) and 32
 runs by a tree: at most (rows + 128) additions, and 32 operations on each term:
 (rows + 160) * 2^-24 * sum |term|."""
 from __future__ import annotations
