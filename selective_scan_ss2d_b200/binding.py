@@ -8,6 +8,7 @@ There is no CPU fallback: if the library is missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -526,6 +527,16 @@ def _raw_stream(device, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Makes a call's new tensors, and fills them, on the stream that the call runs on."""
+    if stream is None:
+        return _HERE
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+
+
 def _token_stride(t, name):
     """Values between tokens of (..., tokens, heads, size): packed heads, tokens at
     any stride (slices of one projection), batches of whole token runs."""
@@ -608,14 +619,15 @@ def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=No
     sdims = (nseq, H, DK, DV)
     if h0 is not None:
         _like(h0, sdims, torch.float32, q.device, "h0")
-    if o is None:
-        o = _new(v, v.dtype)
-    else:
+    if o is not None:
         _like(o, v.shape, q.dtype, q.device, "o")
     if h_last is not None:
         _like(h_last, sdims, torch.float32, q.device, "h_last")
-    elif final_state:
-        h_last = torch.empty(sdims, dtype=torch.float32, device=q.device)
+    with _on(q.device, stream):
+        if o is None:
+            o = _new(v, v.dtype)
+        if h_last is None and final_state:
+            h_last = torch.empty(sdims, dtype=torch.float32, device=q.device)
     rc = lib().gated_delta_rule_fwd(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(h0), _raw(o),
                                     _raw(h_last), _raw(cu_seqlens), nseq, L, *dims, *strides,
                                     DK ** -0.5 if scale is None else float(scale), int(reverse), dt,
@@ -645,12 +657,13 @@ def gated_delta_rule_bwd(q, k, v, g, beta, do, h0=None, dh_last=None, *, scale=N
             _like(t, sdims, torch.float32, q.device, n)
     # packed tokens may leave rows that belong to no sequence: their gradient is zero
     new = torch.empty if cu_seqlens is None else torch.zeros
-    gr = dict(dq=new(q.shape, dtype=q.dtype, device=q.device),
-              dk=new(q.shape, dtype=q.dtype, device=q.device),
-              dv=new(v.shape, dtype=q.dtype, device=q.device),
-              dg=new(g.shape, dtype=torch.float32, device=q.device),
-              dbeta=new(g.shape, dtype=torch.float32, device=q.device),
-              dh0=torch.empty(sdims, dtype=torch.float32, device=q.device) if h0 is not None else None)
+    with _on(q.device, stream):
+        gr = dict(dq=new(q.shape, dtype=q.dtype, device=q.device),
+                  dk=new(q.shape, dtype=q.dtype, device=q.device),
+                  dv=new(v.shape, dtype=q.dtype, device=q.device),
+                  dg=new(g.shape, dtype=torch.float32, device=q.device),
+                  dbeta=new(g.shape, dtype=torch.float32, device=q.device),
+                  dh0=torch.empty(sdims, dtype=torch.float32, device=q.device) if h0 is not None else None)
     rc = lib().gated_delta_rule_bwd(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(h0), _raw(do),
                                     _raw(dh_last), *[_raw(gr[n]) for n in DELTA_GRAD_NAMES],
                                     _raw(cu_seqlens), nseq, L, *dims, *strides,
@@ -676,7 +689,8 @@ def gated_delta_rule_step(q, k, v, g, beta, state, slots=None, *, scale=None, o=
     if slots is not None:
         _like(slots, (B,), torch.int32, q.device, "slots")
     if o is None:
-        o = _new(v, v.dtype)
+        with _on(q.device, stream):
+            o = _new(v, v.dtype)
     else:
         _like(o, v.shape, q.dtype, q.device, "o")
     rc = lib().gated_delta_rule_step(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(state),
@@ -690,13 +704,13 @@ def gated_delta_rule_step(q, k, v, g, beta, state, slots=None, *, scale=None, o=
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
-def _norm_rows(t, like, name):
+def _norm_rows(t, name):
     """(group, stride) of a tensor of rows: contiguous, or (M, G, D) / (M, D)
     with contiguous groups of G rows at any stride (a slice of a projection)."""
     if t.is_contiguous():
         return None
     D = t.shape[-1]
-    if t.dim() not in (2, 3) or t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != D) \
+    if t.dim() not in (2, 3) or t.stride(-1) != 1 or (t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != D) \
             or t.stride(0) < t.shape[-2 if t.dim() == 3 else -1] * (D if t.dim() == 3 else 1):
         raise ValueError(f"{name} must be contiguous, or (M, D) or (M, G, D) with packed rows")
     return (t.shape[1] if t.dim() == 3 else 1), t.stride(0)
@@ -724,8 +738,8 @@ def _norm_prepare(x, z, vectors, post, pre, rdt, what):
         if t is not None and (t.dtype != torch.float32 or t.shape != (D,) or not t.is_cuda or
                               t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{n} must be a contiguous float32 tensor of shape {(D,)} on x's device")
-    lx = _norm_rows(x, x, "x")
-    lz = _norm_rows(z, x, "z") if z is not None else None
+    lx = _norm_rows(x, "x")
+    lz = _norm_rows(z, "z") if z is not None else None
     group = (lx or lz or (1, D))[0]
     xs, zs = (lx or (0, group * D))[1], (lz or (0, group * D))[1]
     return (x.numel() // D if D else 0), D, group, xs, zs, how
@@ -763,16 +777,17 @@ def block_norm_fwd(x, *, z=None, r=None, s=None, post="none", w_post=None, b_pos
         post, pre, rdt, "block_norm_fwd")
     if r is not None:
         _rows_like(r, x, rdt, "r")
-    if r_out is None:
-        r_out = _new(x, rdt)
-    else:
+    if r_out is not None:
         _rows_like(r_out, x, rdt, "r_out")
     if pre == "none":
         y = None
-    elif y is None:
-        y = _new(x, x.dtype)
-    else:
+    elif y is not None:
         _rows_like(y, x, x.dtype, "y")
+    with _on(x.device, stream):
+        if r_out is None:
+            r_out = _new(x, rdt)
+        if y is None and pre != "none":
+            y = _new(x, x.dtype)
     rc = lib().block_norm_fwd(_raw(x), _raw(z), _raw(r), _raw(s), _raw(w_post), _raw(b_post),
                               _raw(w_pre), _raw(b_pre), _raw(r_out), _raw(y), rows, D, group, xs,
                               zs, *how, eps, _DTYPES[x.dtype], _DTYPES[rdt],
@@ -809,8 +824,9 @@ def block_norm_bwd(x, dr_out, dy=None, *, r_out=None, z=None, s=None, post="none
     if dr_out is not None:
         _rows_like(dr_out, x, rdt, "dr_out")
     post_w, pre_w = (w_post, b_post) if post != "none" else (None, None), (w_pre, b_pre) if has_pre else (None, None)
-    vec = [None if t is None else torch.empty_like(t) for t in (s, *post_w, *pre_w)]
-    g = (_new(x, x.dtype), None if z is None else _new(x, x.dtype), _new(x, rdt) if residual else None, *vec)
+    with _on(x.device, stream):
+        vec = [None if t is None else torch.empty_like(t) for t in (s, *post_w, *pre_w)]
+        g = (_new(x, x.dtype), None if z is None else _new(x, x.dtype), _new(x, rdt) if residual else None, *vec)
     rc = lib().block_norm_bwd(_raw(x), _raw(z), _raw(r_out) if has_pre else None, _raw(s),
                               _raw(w_post), _raw(b_post), _raw(w_pre), _raw(dr_out),
                               _raw(dy) if has_pre else None, *map(_raw, g), rows, D, group, xs, zs,

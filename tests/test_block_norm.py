@@ -306,6 +306,25 @@ def test_slices_of_a_projection(off):
 
 
 @pytest.mark.gpu
+def test_rows_past_32_bits_and_groups_of_one():
+    """rows 2^24 values apart: the bits of packed ones; so are groups of one row, whatever their own stride"""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, z, d = (torch.randn(140, 64, device="cuda", generator=g).bfloat16() for _ in range(3))
+    far = torch.empty(140, 1 << 24, dtype=torch.bfloat16, device="cuda")
+    fx, fz = far[:, :64], far[:, 64:128]
+    fx.copy_(x)
+    fz.copy_(z)
+    want, _ = binding.block_norm_fwd(x, z=z, post="rms")
+    back = binding.block_norm_bwd(x, d, z=z, post="rms")
+    for a, b, view in ((fx, fz, (140, 64)), (fx[:, None], fz[:, None], (140, 1, 64))):
+        assert not a.is_contiguous()
+        got, _ = binding.block_norm_fwd(a, z=b, post="rms")
+        grad = binding.block_norm_bwd(a, d.view(view), z=b, post="rms")
+        assert torch.equal(got.view(140, 64), want)
+        assert all(torch.equal(grad[n].view(140, 64), back[n]) for n in ("dx", "dz"))
+
+
+@pytest.mark.gpu
 def test_in_place_residual_stream_and_capture():
     a = make(64, 192, "none", "layer")
     t, _ = dev(a, "bf16", "f32")

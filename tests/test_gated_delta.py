@@ -527,6 +527,50 @@ def test_repeatable_streams_and_graphs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_another_stream_than_the_current_one(raw):
+    """everything that a call writes, rows of no sequence among it, is written on its stream"""
+    t, _ = dev(make(1, 150, 1, 2, 32, 32), "bf16")
+    do = torch.ones_like(t["v"])
+    cu = torch.tensor([7, 60, 120], dtype=torch.int32).cuda()
+    want = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)   # the current stream is behind for some 25 ms
+    got = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu, stream=s.cuda_stream if raw else s)
+    torch.cuda.synchronize()
+    assert all(got[n] is None or torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """tokens 2^24 values apart, and a state that begins past 2^31 values of the pool: the bits of packed ones"""
+    t, _ = dev(make(1, 135, 1, 1, 16, 32), "bf16")
+    do = torch.ones_like(t["v"])
+    far = torch.empty(135, 1, 1 << 24, dtype=torch.bfloat16, device="cuda")
+    wide = dict(t)
+    for n, at, w in (("q", 0, 16), ("k", 16, 16), ("v", 32, 32)):
+        wide[n] = far[None, :, :, at:at + w]
+        wide[n].copy_(t[n])
+    assert wide["v"].stride(1) * 134 > 2 ** 31
+    o, h = binding.gated_delta_rule_fwd(**t, final_state=True)
+    o1, h1 = binding.gated_delta_rule_fwd(**wide, final_state=True)
+    g, g1 = (binding.gated_delta_rule_bwd(**u, do=do) for u in (t, wide))
+    assert torch.equal(o, o1) and torch.equal(h, h1)
+    assert all(g[n] is None or torch.equal(g[n], g1[n]) for n in g)
+    del far, wide
+    n = (1 << 31) // (16 * 32) + 2
+    pool = torch.empty(n, 1, 16, 32, device="cuda")
+    small = torch.ones(2, 1, 16, 32, device="cuda")
+    pool[-2:] = 1
+    one = {k: v[0, :2] for k, v in t.items()}
+    slots = torch.tensor([n - 1, n - 2], dtype=torch.int32).cuda()
+    o2 = binding.gated_delta_rule_step(**one, state=pool, slots=slots)
+    o3 = binding.gated_delta_rule_step(**one, state=small, slots=torch.tensor([1, 0], dtype=torch.int32).cuda())
+    assert torch.equal(o2, o3) and torch.equal(pool[-2:], small)
+
+
+@pytest.mark.gpu
 def test_a_block_of_them_together():
     """Pre-norm -> q, k normalised by the block norm -> delta rule -> gated norm -> residual + next norm, and back,
     against the oracles' chain in float64 (float32 inputs, so that only float32 rounding is between them)."""
