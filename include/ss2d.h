@@ -410,7 +410,7 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * sequence of no tokens gets h_last = h0.
  * All pointers DEVICE pointers of the current device (SS2D_ERR_PTR otherwise),
  * 16-byte aligned.  Asynchronous on `stream`; scratch (per 64 tokens and head 21 to
- * 31 KB, for float16 and float32 also 512 or 768 DKP bytes per key head, DKP = 64 or
+ * 32 KB, for float16 and float32 also 512 or 768 DKP bytes per key head, DKP = 64 or
  * 128, DK rounded up; for few long sequences three states per head and segment) comes
  * from the stream-ordered pool.  L < 2^31 - 64.
  *
@@ -432,7 +432,7 @@ int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const floa
  * a fixed order; dg, dbeta (tokens, H) float32; dh0 (nseq, H, DK, DV) float32 or NULL
  * (not wanted; may be dh_last).  The forward's other arguments and rules hold.
  * The states are computed again from the inputs and kept in scratch: per 64 tokens
- * and head 8 * DKP * DV + 512 * DV + 31488 bytes besides the forward's, from the
+ * and head 8 * DKP * DV + 512 * DV + 32000 bytes besides the forward's, from the
  * stream-ordered pool.  No atomics: the same bits on every call. */
 int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const float *g,
                          const float *beta, const float *h0, const void *dout,

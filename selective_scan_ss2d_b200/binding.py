@@ -655,15 +655,12 @@ def gated_delta_rule_bwd(q, k, v, g, beta, do, h0=None, dh_last=None, *, scale=N
     for t, n in ((h0, "h0"), (dh_last, "dh_last")):
         if t is not None:
             _like(t, sdims, torch.float32, q.device, n)
-    # packed tokens may leave rows that belong to no sequence: their gradient is zero
-    new = torch.empty if cu_seqlens is None else torch.zeros
     with _on(q.device, stream):
-        gr = dict(dq=new(q.shape, dtype=q.dtype, device=q.device),
-                  dk=new(q.shape, dtype=q.dtype, device=q.device),
-                  dv=new(v.shape, dtype=q.dtype, device=q.device),
-                  dg=new(g.shape, dtype=torch.float32, device=q.device),
-                  dbeta=new(g.shape, dtype=torch.float32, device=q.device),
+        gr = dict(dq=_new(q, q.dtype), dk=_new(k, q.dtype), dv=_new(v, q.dtype), dg=_new(g, g.dtype),
+                  dbeta=_new(g, g.dtype),
                   dh0=torch.empty(sdims, dtype=torch.float32, device=q.device) if h0 is not None else None)
+        if cu_seqlens is not None:   # packed tokens may leave rows that belong to no sequence: their gradient is zero
+            torch._foreach_zero_([gr[n] for n in DELTA_GRAD_NAMES[:5]])
     rc = lib().gated_delta_rule_bwd(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(h0), _raw(do),
                                     _raw(dh_last), *[_raw(gr[n]) for n in DELTA_GRAD_NAMES],
                                     _raw(cu_seqlens), nseq, L, *dims, *strides,

@@ -129,7 +129,7 @@ int run_chunked(Call &c, bool bwd)
     const size_t kp = pl.npi > 1 ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
     const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
     const size_t ns = segs * p.H * p.DV * pl.dkp * 4;
-    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * 3 * kDeltaC * 4, sx, sx, vx, vx, ns, ns, bwd ? ns : 0, bwd ? ns : 0,
+    const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * ss2d::kDeltaVec * 4, sx, sx, vx, vx, ns, ns, bwd ? ns : 0, bwd ? ns : 0,
                            segs * p.H * 3 * pl.dkp * pl.dkp * 2};
     size_t off[14], total = 0;
     for (int i = 0; i < 14; ++i) {

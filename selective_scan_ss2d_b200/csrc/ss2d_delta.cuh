@@ -42,6 +42,7 @@ constexpr int kDeltaMaxDK = 128;
 constexpr int kDeltaMaxDV = 256;
 // exp(g) of anything below is 0 in float32; a finite floor keeps sums of g finite (g = -inf forgets all)
 constexpr float kDeltaGFloor = -200.f;
+constexpr int kDeltaVec = 5 * kDeltaC;   // floats of `vec` per (slot, head)
 
 struct DeltaParams {
     const void *q, *k, *v;         // token rows: HK x DK (q, k), H x DV (v)
@@ -64,7 +65,7 @@ struct DeltaParams {
     long long nslots;
     void *kp, *qp;                 // bf16 parts of k and q per (slot, key head): [NPI][64][DKP]
     void *Tp, *Pp;                 // bf16 parts of T and P per (slot, head), packed blocks
-    float *vec;                    // per (slot, head): e^c, e^{c_last - c}, beta (64 each)
+    float *vec;                    // per (slot, head): e^c, e^{c_last - c}, beta, c log2(e) and what it lacks (64 each)
     // segments of a long chain: SC chunks each (0: none)
     int SC;
     float *Ns, *dNs;               // S^T at a segment's end from zero, dS^T at its start: [DV][DKP] per (segment, head)
@@ -340,16 +341,21 @@ __device__ __forceinline__ void mma_rows(float (&c0)[4], float (&c1)[4], const u
     mma_parts<NA, NL, KEEP>(c0, c1, a, b);
 }
 // B from a [k][n] tile: rows k, columns n
+template <int RB, int N>
+__device__ __forceinline__ void frag_cols(uint32_t tile, int part, int row, int piece, uint32_t (&b)[N][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+        ldsm4t(tile + m * part + swz<RB>(row + (lane & 15), piece + (lane >> 4)), b[m]);
+}
 template <int RB, int NA, int NB, int KEEP>
 __device__ __forceinline__ void mma_cols(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], uint32_t tile,
                                          int part, int row, int piece)
 {
     constexpr int NL = NB < KEEP ? NB : KEEP;
-    const int lane = threadIdx.x & 31;
     uint32_t b[NL][4];
-#pragma unroll
-    for (int m = 0; m < NL; ++m)
-        ldsm4t(tile + m * part + swz<RB>(row + (lane & 15), piece + (lane >> 4)), b[m]);
+    frag_cols<RB, NL>(tile, part, row, piece, b);
     mma_parts<NA, NL, KEEP>(c0, c1, a, b);
 }
 
@@ -763,10 +769,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
         const long long sh = (long long)blockIdx.x * p.H + h;
         __syncthreads();   // the tiles (or the last head's T) are read, the decays are here
         if (tid < kDeltaC) {
-            float *vec = p.vec + sh * 3 * kDeltaC;
+            float *vec = p.vec + sh * kDeltaVec;
             vec[tid] = delta_decay(ch[tid], cl[tid]);
             vec[kDeltaC + tid] = delta_decay(ch[kDeltaC - 1] - ch[tid], cl[kDeltaC - 1] - cl[tid]);
             vec[2 * kDeltaC + tid] = be[tid];
+            vec[3 * kDeltaC + tid] = ch[tid];
+            vec[4 * kDeltaC + tid] = cl[tid];
         }
         const int ir = lane >> 2, jr = (lane & 3) * 2;   // row and first column of a lane in an 8 x 8 tile
 #pragma unroll

@@ -136,7 +136,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                 cp16(base + Lay::oV + dst, src + (on ? d : 0), on);
             }
             if (tid < 3 * kDeltaC * 4 / 16)
-                cp16(base + Lay::oX + tid * 16, p.vec + sh * 3 * kDeltaC + tid * 4, true);
+                cp16(base + Lay::oX + tid * 16, p.vec + sh * kDeltaVec + tid * 4, true);
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         };
         // V or dO of the warp's columns and 16 tokens, transposed, in accumulator layout

@@ -16,14 +16,18 @@
 // gradients of shared keys and queries are sums in a fixed order: warp w
 // holds rows 16 (w % 4) .. + 15 and half w / 4 of the columns of dq, dk (over DK)
 // and of dP, dA (over tokens).  DV is gone through in tiles of 32 columns:
-// the float32 tiles of S, dS, dX and V' are copied asynchronously while the tile
-// before is multiplied, and split into bf16 parts when they are here.  What reaches a
+// the tiles of S, dS, dX, V', dO and V are copied asynchronously while the tile
+// before is multiplied, and split into bf16 parts when they are here (dX.V is summed
+// from the copies).  What reaches a
 // float32 output through dg and dbeta keeps three parts; the products with GP and
 // GA two when dq and dk are stored in 16 bits.  Rows of tokens behind the end take no part.
 //
 // Heads of up to 64 in bfloat16 run two CTAs per SM (128 registers): with one, the kernel
 // stood at 16 % of the tensor pipe, waiting on its staging (808 us for 6144
-// chunks of 64 x 64 heads).
+// chunks of 64 x 64 heads).  With two it took 412; of a CTA's 37,000 clocks the products
+// had 16,000, the sums of E 6,500, most of them in branches, and staging 4,500: a tile of
+// S^T or V' read once for two products, selects in place of the branches and dc
+// and dbeta by two warps made it 364 (31,000 clocks; the tensor pipe at 38 %).
 #pragma once
 
 #include "ss2d_delta_chain.cuh"
@@ -36,7 +40,7 @@ template <typename Tin, int DKP>
 struct GradLayout {
     static constexpr int NPI = DeltaParts<Tin>::n, NPG = sizeof(Tin) == 2 ? 2 : 3;
     static constexpr int DVB = sizeof(Tin) == 4 && DKP == 128 ? 16 : 32;   // DV columns per staged tile
-    static constexpr int ORow = DVB * 2 + 16;        // bytes of a staged row of dO or V
+    static constexpr int ORow = DVB * 2 + 16;        // bytes of a staged row of dO
     static constexpr int RBK = DKP * 2, PBK = kDeltaC * RBK;
     static constexpr int SB = DVB * RBK;             // one part of S^T or dS^T
     static constexpr int XB = DVB * 128;             // one part of dX, V'
@@ -44,12 +48,15 @@ struct GradLayout {
     static constexpr int sG = 2 * NPG * kTriBytes;   // GP and GA, in the place of S^T and dS^T
     static constexpr int sS = 6 * SB > sG ? 6 * SB : sG;
     static constexpr int oO = oS + sS;
-    static constexpr int oU = oO + NPI * kDeltaC * ORow;   // V
-    static constexpr int oX = oU + NPI * kDeltaC * ORow;
+    static constexpr int oX = oO + NPI * kDeltaC * ORow;
     static constexpr int oV = oX + 3 * XB;
-    static constexpr int oR = oV + 3 * XB;           // the next tile as it is: S^T, dS^T, dX, V'
-    static constexpr int rS = DVB * DKP * 4, rX = DVB * kDeltaC * 4;
-    static constexpr int bytes = oR + 2 * rS + 2 * rX;
+    static constexpr int oR = oV + 3 * XB;           // the next tile as it is: S^T, dS^T, dX, V', dO, V
+    static constexpr int rS = DVB * DKP * 4, rX = DVB * kDeltaC * 4, rO = DVB * kDeltaC * (int)sizeof(Tin);
+    static constexpr int PO = DVB * (int)sizeof(Tin) / 16;   // 16-byte pieces of a raw row of dO or V
+    static constexpr int bytes = oR + 2 * rS + 2 * rX + 2 * rO;
+    static constexpr int oE = oX;                    // sums of E, in the place of dX
+    // place of piece pc of token t in a raw tile of dO or V: eight tokens' same pieces in eight bank groups
+    static __device__ __forceinline__ int piece(int t, int pc) { return t * PO + (pc ^ (t / (8 / PO) & (PO - 1))); }
 };
 
 // 8 floats as the parts of a swizzled row piece
@@ -76,31 +83,37 @@ __device__ __forceinline__ void load8(const float *src, float (&v)[8])
     v[6] = b.z;
     v[7] = b.w;
 }
-// 8 input values as the parts of a row piece, parts `part` bytes apart, zeros where not `in`; asynchronously where
-// the input is its own part
-template <typename Tin, int NPI>
-__device__ __forceinline__ void put_inputs(unsigned char *dst, int part, const Tin *row, bool in)
-{
-    if constexpr (NPI == 1) {
-        cp16(smem_addr(dst), row, in);
-    } else {
-        float v[8];
+// 8 input values of a raw tile
+template <typename Tin>
+struct Piece8 {
+    static constexpr int n = sizeof(Tin) / 2;
+    uint4 u[n];
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = 0.f;
-        if (in) {
-            if constexpr (sizeof(Tin) == 4) {
-                load8(row, v);
-            } else {
-                const uint4 u = *reinterpret_cast<const uint4 *>(row);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int i = 0; i < n; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (n == 2) {
+                    v[4 * i + j] = __uint_as_float(w[j]);
+                } else {
                     v[2 * j] = half_bits_to_f32<Tin>(w[j] & 0xffffu);
                     v[2 * j + 1] = half_bits_to_f32<Tin>(w[j] >> 16);
                 }
             }
         }
+    }
+};
+// the parts of such a piece, `part` bytes apart
+template <typename Tin, int NPI>
+__device__ __forceinline__ void put_piece(unsigned char *dst, int part, const Piece8<Tin> &p)
+{
+    if constexpr (NPI == 1) {
+        *reinterpret_cast<uint4 *>(dst) = p.u[0];
+    } else {
+        float v[8];
+        p.get(v);
         uint32_t w[4][NPI];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -113,17 +126,19 @@ __device__ __forceinline__ void put_inputs(unsigned char *dst, int part, const T
 
 // SHARED: several value heads share the key head
 template <typename Tin, int DKP, bool SHARED>
-__global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 107 * 1024 ? 2 : 1))
+__global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 109 * 1024 ? 2 : 1))
     delta_grad_kernel(const DeltaParams p)
 {
     using Lay = GradLayout<Tin, DKP>;
     constexpr int NPI = Lay::NPI, NPG = Lay::NPG, RBK = Lay::RBK, PBK = Lay::PBK, DVB = Lay::DVB;
     constexpr int NH = DKP / 16;   // 8-column tiles of a warp's half of DK
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ __align__(16) float vec[3 * kDeltaC];   // e^c, e^{c_last - c}, beta
-    __shared__ float ch[kDeltaC], cl[kDeltaC], be[kDeltaC];
-    __shared__ float xv[kDeltaC], rowR[2][kDeltaC], rsd[8];
-    __shared__ float rowE[2][kDeltaC], rowB[2][kDeltaC], rowQ[2][kDeltaC], rowK[2][kDeltaC], colE[4][kDeltaC];
+    __shared__ __align__(16) float vec[kDeltaVec];   // e^c, e^{c_last - c}, beta, c and what it lacks
+    const float *be = vec + 2 * kDeltaC, *ch = vec + 3 * kDeltaC, *cl = vec + 4 * kDeltaC;
+    __shared__ float xv[4][kDeltaC], rowR[2][kDeltaC], rsd[8];
+    __shared__ float rowQ[2][kDeltaC], rowK[2][kDeltaC];
+    float(*rowE)[kDeltaC] = reinterpret_cast<float(*)[kDeltaC]>(dsm + Lay::oE), (*rowB)[kDeltaC] = rowE + 2,
+    (*colE)[kDeltaC] = rowE + 4;
     int s, c;
     DeltaSeq q;
     if (!delta_slot(p, blockIdx.x, s, q, c))
@@ -135,11 +150,11 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
     const bool act = wr < nb;
     const uint32_t sa = smem_addr(dsm);
     const int tiles = (p.DV + DVB - 1) / DVB;
-    // copies the raw tile n (head by head) of the group: S^T, dS^T, dX, V', rows past DV zero
-    auto raw = [&](int n) {
+    // copies the raw tile n (head by head) of the group, rows past DV zero: S^T and dS^T; dX, V', dO and V
+    auto raw_states = [&](int n) {
         const long long sh = (long long)blockIdx.x * p.H + hk * G + n / tiles;
         const int d0 = n % tiles * DVB;
-        constexpr int PS = DKP / 4, PX = kDeltaC / 4;   // 16-byte pieces of a row
+        constexpr int PS = DKP / 4;   // 16-byte pieces of a row
 #pragma unroll 4
         for (int i = tid; i < DVB * PS; i += kGradThreads) {
             const bool on = d0 + i / PS < p.DV;
@@ -147,6 +162,11 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
             cp16(sa + Lay::oR + i * 16, p.Sx + o, on);
             cp16(sa + Lay::oR + Lay::rS + i * 16, p.dSx + o, on);
         }
+    };
+    auto raw_tokens = [&](int n) {
+        const long long sh = (long long)blockIdx.x * p.H + hk * G + n / tiles;
+        const int d0 = n % tiles * DVB;
+        constexpr int PX = kDeltaC / 4;
 #pragma unroll 2
         for (int i = tid; i < DVB * PX; i += kGradThreads) {
             const bool on = d0 + i / PX < p.DV;
@@ -154,10 +174,20 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
             cp16(sa + Lay::oR + 2 * Lay::rS + i * 16, p.dXx + o, on);
             cp16(sa + Lay::oR + 2 * Lay::rS + Lay::rX + i * 16, p.Vx + o, on);
         }
+        const int h = hk * G + n / tiles;
+        for (int i = tid; i < kDeltaC * Lay::PO; i += kGradThreads) {
+            const int t = i / Lay::PO, pc = i % Lay::PO, d = d0 + pc * (16 / (int)sizeof(Tin));
+            const bool on = t0 + t < q.len && d < p.DV;
+            const long long tok = delta_token(p, q, on ? t0 + t : 0);
+            const uint32_t at = sa + Lay::oR + 2 * Lay::rS + 2 * Lay::rX + Lay::piece(t, pc) * 16;
+            cp16(at, static_cast<const Tin *>(p.dout) + (tok * p.H + h) * p.DV + (on ? d : 0), on);
+            cp16(at + Lay::rO, static_cast<const Tin *>(p.v) + tok * p.vs + (long long)h * p.DV + (on ? d : 0), on);
+        }
     };
     delta_stage_parts<Tin, DKP, NPI, kGradThreads>(p, p.k, p.ks, hk, q, t0, dsm + Lay::oK);
     delta_stage_parts<Tin, DKP, NPI, kGradThreads>(p, p.q, p.qs, hk, q, t0, dsm + Lay::oQ);
-    raw(0);
+    raw_states(0);
+    raw_tokens(0);
     float dqt[SHARED ? NH : 1][4], dkt[SHARED ? NH : 1][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -165,6 +195,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
         for (int n = 0; n < (SHARED ? NH : 1); ++n)
             dqt[n][j] = dkt[n][j] = 0.f;
     }
+    const int ft = tid & 63, fp = tid >> 6;   // a thread's piece of dO and V: 8 columns from fp * 8 of token ft
     const int i0 = wr * 16 + g8;   // the lane's rows: i0, i0 + 8
     // the lane's two values of row i, tile nt of its half, of the staged q or k
     auto pair = [&](int tile, int i, int nt) {
@@ -183,11 +214,9 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
         const int h = hk * G + hi;
         const long long sh = (long long)blockIdx.x * p.H + h;
         __syncthreads();
-        if (warp == 0)
-            delta_decays(p, q, t0, h, ch, cl, be);
-        if (tid >= 64)
-            vec[tid - 64] = p.vec[sh * 3 * kDeltaC + tid - 64];
-        float dk2[NH][4], dP[4][4], dA[4][4], xd[2][4], sd = 0.f;
+        if (tid < kDeltaVec / 4)
+            cp16(smem_addr(vec) + tid * 16, p.vec + sh * kDeltaVec + tid * 4, true);
+        float dk2[NH][4], dP[4][4], dA[4][4], xd = 0.f, sd = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -196,23 +225,28 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
 #pragma unroll
             for (int n = 0; n < NH; ++n)
                 dq[n][j] = dk[n][j] = dk2[n][j] = 0.f;
-            xd[0][j] = xd[1][j] = 0.f;
         }
         const int tr = tid >> 3, tk = (tid & 7) * 8;   // a thread's piece of a token tile: 8 tokens from tk of row tr
         for (int ti = 0; ti < tiles; ++ti) {
-            const int d0 = ti * DVB;
             cp_wait();
             __syncthreads();   // the raw tile is here, the last tile's parts are read
-            for (int i = tid; i < kDeltaC * (DVB / 8); i += kGradThreads) {   // dO and V, rows of DVB columns
-                const int r = i / (DVB / 8), pc = i % (DVB / 8), t = t0 + r, d = d0 + pc * 8;
-                const bool in = t < q.len && d < p.DV;
-                const long long tok = delta_token(p, q, in ? t : 0);
-                const Tin *od = static_cast<const Tin *>(p.dout) + (tok * p.H + h) * p.DV + (in ? d : 0);
-                const Tin *vd = static_cast<const Tin *>(p.v) + tok * p.vs + (long long)h * p.DV + (in ? d : 0);
-                put_inputs<Tin, NPI>(dsm + Lay::oO + r * Lay::ORow + pc * 16, kDeltaC * Lay::ORow, od, in);
-                put_inputs<Tin, NPI>(dsm + Lay::oU + r * Lay::ORow + pc * 16, kDeltaC * Lay::ORow, vd, in);
-            }
             const float *rs = reinterpret_cast<const float *>(dsm + Lay::oR);
+            if (fp < DVB / 8) {
+                const uint4 *ro = reinterpret_cast<const uint4 *>(rs + Lay::rS / 2 + Lay::rX / 2);
+                Piece8<Tin> u;
+#pragma unroll
+                for (int i = 0; i < u.n; ++i)
+                    u.u[i] = ro[Lay::piece(ft, fp * u.n + i)];
+                put_piece<Tin, NPI>(dsm + Lay::oO + ft * Lay::ORow + fp * 16, kDeltaC * Lay::ORow, u);
+#pragma unroll
+                for (int i = 0; i < u.n; ++i)
+                    u.u[i] = ro[Lay::rO / 16 + Lay::piece(ft, fp * u.n + i)];
+                float x[8];
+                u.get(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    xd = fmaf(rs[Lay::rS / 2 + (fp * 8 + j) * kDeltaC + ft], x[j], xd);
+            }
             for (int i = tid; i < DVB * (DKP / 8); i += kGradThreads) {
                 const int r = i / (DKP / 8), pc = i % (DKP / 8);
                 float a[8], b[8];
@@ -231,52 +265,35 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                 load8(rs + Lay::rS / 2 + Lay::rX / 4 + tr * kDeltaC + tk, x);
                 put_parts<3, 128>(dsm + Lay::oV, Lay::XB, tr, tid & 7, x);
             }
-            cp_wait();
             __syncthreads();   // the parts are here, the raw tile is free
-            if (hi * tiles + ti + 1 < G * tiles)
-                raw(hi * tiles + ti + 1);
-            if (act) {
+            const bool more = hi * tiles + ti + 1 < G * tiles;
+            if (more)
+                raw_states(hi * tiles + ti + 1);
 #pragma unroll
-                for (int ks = 0; ks < DVB / 16; ++ks) {
+            for (int ks = 0; ks < DVB / 16; ++ks) {
+                if (act) {
                     {
-                        uint32_t ao[NPI][4];
+                        // a tile of S^T serves dq and dk, one of V' dP and dA
+                        uint32_t ao[NPI][4], ax[3][4], b[3][4];
 #pragma unroll
                         for (int n = 0; n < NPI; ++n)
                             ldsm4(sa + Lay::oO + (n * kDeltaC + wr * 16 + (lane & 15)) * Lay::ORow +
                                       (ks * 2 + (lane >> 4)) * 16,
                                   ao[n]);
-#pragma unroll
-                        for (int nt = 0; nt < NH; nt += 2)
-                            mma_cols<RBK, NPI, 3, 3>(dq[nt], dq[nt + 1], ao, sa + Lay::oS, Lay::SB, ks * 16,
-                                                     wc * NH + nt);
-#pragma unroll
-                        for (int nt = 0; nt < 4; nt += 2)
-                            if (wc * 2 + nt / 2 <= wr)   // blocks above the diagonal are not needed
-                                mma_cols<128, NPI, 3, 3>(dP[nt], dP[nt + 1], ao, sa + Lay::oV, Lay::XB, ks * 16,
-                                                         wc * 4 + nt);
-                    }
-                    {
-                        uint32_t ax[3][4];
                         frag_t<3>(sa + Lay::oX, Lay::XB, ks * 16, wr * 16, ax);
 #pragma unroll
-                        for (int nt = 0; nt < 4; nt += 2)
-                            if (wc * 2 + nt / 2 <= wr)
-                                mma_cols<128, 3, 3, 3>(dA[nt], dA[nt + 1], ax, sa + Lay::oV, Lay::XB, ks * 16,
-                                                       wc * 4 + nt);
-#pragma unroll
-                        for (int nt = 0; nt < NH; nt += 2)
-                            mma_cols<RBK, 3, 3, 3>(dk[nt], dk[nt + 1], ax, sa + Lay::oS, Lay::SB, ks * 16,
-                                                   wc * NH + nt);
-                        if (wc == 1) {   // the diagonal of dX V^T
-                            uint32_t b[NPI][4];
-#pragma unroll
-                            for (int n = 0; n < NPI; ++n)
-                                ldsm4(sa + Lay::oU +
-                                          (n * kDeltaC + wr * 16 + (lane & 7) + (lane >> 4) * 8) * Lay::ORow +
-                                          (ks * 2 + (lane >> 3 & 1)) * 16,
-                                      b[n]);
-                            mma_parts<3, NPI, 3>(xd[0], xd[1], ax, b);
+                        for (int nt = 0; nt < NH; nt += 2) {
+                            frag_cols<RBK, 3>(sa + Lay::oS, Lay::SB, ks * 16, wc * NH + nt, b);
+                            mma_parts<NPI, 3, 3>(dq[nt], dq[nt + 1], ao, b);
+                            mma_parts<3, 3, 3>(dk[nt], dk[nt + 1], ax, b);
                         }
+#pragma unroll
+                        for (int nt = 0; nt < 4; nt += 2)
+                            if (wc * 2 + nt / 2 <= wr) {   // blocks above the diagonal are not needed
+                                frag_cols<128, 3>(sa + Lay::oV, Lay::XB, ks * 16, wc * 4 + nt, b);
+                                mma_parts<NPI, 3, 3>(dP[nt], dP[nt + 1], ao, b);
+                                mma_parts<3, 3, 3>(dA[nt], dA[nt + 1], ax, b);
+                            }
                     }
                     {
                         uint32_t av[3][4];
@@ -287,16 +304,16 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                                                    ks * 16, wc * NH + nt);
                     }
                 }
+                // between the products: all copies at once in front of them held up their ldmatrix
+                if (ks == 0 && more)
+                    raw_tokens(hi * tiles + ti + 1);
             }
         }
         for (int m = 1; m < 32; m <<= 1)
             sd += __shfl_xor_sync(0xffffffffu, sd, m);
         if (lane == 0)
             rsd[warp] = sd;
-        if (wc == 1 && t2 == (g8 & 6)) {   // row g8 + 8 hf, column the same
-            xv[i0] = g8 & 1 ? xd[0][1] : xd[0][0];
-            xv[i0 + 8] = g8 & 1 ? xd[1][3] : xd[1][2];
-        }
+        xv[fp][ft] = xd;
         // dq's first term and its product with q; dk's two and theirs with k
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -348,33 +365,27 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
         }
         __syncthreads();   // every warp is done with S^T: GP and GA take its place
         unsigned char *gp = dsm + Lay::oS, *ga = gp + NPG * kTriBytes;
-        float re[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f};
+        float re[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f}, ce[8];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int bj = wc * 2 + n / 2, jc = (n & 1) * 8 + t2;
-            float ce[2] = {0.f, 0.f};
+            ce[2 * n] = ce[2 * n + 1] = 0.f;
             if (act && bj <= wr) {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int i = i0 + hf * 8;
                     float vp[2], va[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < 2; ++e) {   // chosen after the arithmetic: branches took twice the time
                         const int j = bj * 16 + jc + e, x = hf * 2 + e;
-                        vp[e] = va[e] = 0.f;
-                        if (j <= i) {
-                            const float D = delta_decay(ch[i] - ch[j], cl[i] - cl[j]);
-                            vp[e] = p.scale * D * dP[n][x];
-                            float E = vp[e] * qk[n][x];
-                            if (j < i) {
-                                const float Dk = D * kk[n][x], da = -dA[n][x];
-                                va[e] = be[i] * D * da;
-                                E = fmaf(be[i] * Dk, da, E);
-                                rb[hf] = fmaf(Dk, da, rb[hf]);
-                            }
-                            re[hf] += E;
-                            ce[e] += E;
-                        }
+                        const float D = delta_decay(ch[i] - ch[j], cl[i] - cl[j]), da = -D * dA[n][x];
+                        const float pp = p.scale * D * dP[n][x], r = j < i ? kk[n][x] * da : 0.f;
+                        vp[e] = j <= i ? pp : 0.f;
+                        va[e] = j < i ? be[i] * da : 0.f;
+                        const float E = j <= i ? fmaf(be[i], r, pp * qk[n][x]) : 0.f;
+                        rb[hf] += r;
+                        re[hf] += E;
+                        ce[2 * n + e] += E;
                     }
                     uint32_t w[NPG];
                     const uint32_t o = tri_block(wr, bj) + tri_piece(g8 + hf * 8, n & 1) + t2 * 2;
@@ -388,14 +399,16 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                         *reinterpret_cast<uint32_t *>(ga + m * kTriBytes + o) = w[m];
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                for (int m = 4; m < 32; m <<= 1)
-                    ce[e] += __shfl_xor_sync(0xffffffffu, ce[e], m);
-                if (g8 == 0)
-                    colE[wr][bj * 16 + jc + e] = ce[e];
-            }
         }
+        // column sums over the eight rows of a lane's group: lane g8 ends with column pair g8 / 2, column g8 % 2
+#pragma unroll
+        for (int m = 4; m; m >>= 1) {
+            const bool up = g8 & m;
+#pragma unroll
+            for (int k = 0; k < m; ++k)
+                ce[k] = (up ? ce[k + m] : ce[k]) + __shfl_xor_sync(0xffffffffu, up ? ce[k] : ce[k + m], 4 * m);
+        }
+        colE[wr][wc * 32 + (g8 >> 1) * 8 + t2 + (g8 & 1)] = ce[0];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             for (int m = 1; m < 4; m <<= 1) {
@@ -408,8 +421,8 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
             }
         }
         __syncthreads();
-        if (warp == 4) {   // the warp with the fewest blocks
-            // dc, dbeta; then sums of dc from the end: lane l holds tokens 2l, 2l + 1
+        // lane l holds tokens 2l, 2l + 1
+        if (warp == 4) {   // dc, and its sums from the end; what the last token has besides goes to all
             float dc[2], kls = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -418,29 +431,33 @@ __global__ void __launch_bounds__(kGradThreads, (GradLayout<Tin, DKP>::bytes <= 
                 kls += kl;
                 const float E = (rowE[0][i] + rowE[1][i]) - ((colE[0][i] + colE[1][i]) + (colE[2][i] + colE[3][i]));
                 dc[e] = ((E + (rowQ[0][i] + rowQ[1][i])) - be[i] * rd) - kl;
-                if (t0 + i < q.len)
-                    p.dbeta[delta_token(p, q, t0 + i) * p.H + h] = (xv[i] - rd) + (rowB[0][i] + rowB[1][i]);
             }
-            for (int m = 1; m < 32; m <<= 1)
-                kls += __shfl_xor_sync(0xffffffffu, kls, m);
-            if (lane == 31) {
-                float t = 0.f;
-                for (int w = 0; w < 8; ++w)
-                    t += rsd[w];
-                dc[1] += kls + vec[kDeltaC - 1] * t;
-            }
-            float sum = dc[0] + dc[1];
+            float t = 0.f, sum = dc[0] + dc[1];
+            for (int w = 0; w < 8; ++w)
+                t += rsd[w];
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
+                kls += __shfl_xor_sync(0xffffffffu, kls, o);
                 const float u = __shfl_down_sync(0xffffffffu, sum, o);
                 if (lane + o < 32)
                     sum += u;
             }
+            const float last = kls + vec[kDeltaC - 1] * t;
             float after = __shfl_down_sync(0xffffffffu, sum, 1);
-            after = (lane < 31 ? after : 0.f) + dc[1];
+            after = ((lane < 31 ? after : 0.f) + dc[1]) + last;
             if (t0 + 2 * lane < q.len)
                 p.dg[delta_token(p, q, t0 + 2 * lane) * p.H + h] = after + dc[0];
             if (t0 + 2 * lane + 1 < q.len)
                 p.dg[delta_token(p, q, t0 + 2 * lane + 1) * p.H + h] = after;
+        } else if (warp == 5) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                if (t0 + i < q.len)
+                    p.dbeta[delta_token(p, q, t0 + i) * p.H + h] =
+                        (((xv[0][i] + xv[1][i]) + (xv[2][i] + xv[3][i])) - (rowR[0][i] + rowR[1][i])) +
+                        (rowB[0][i] + rowB[1][i]);
+            }
         }
         // GP K into dq; GP^T Q, GA K, GA^T K into dk
         if (act) {

@@ -108,7 +108,7 @@ __device__ __forceinline__ void delta_split(const DeltaParams &p, int tile, bool
             load_rows(c, sm0 + Lay::oK + (KBUF == 2 ? i & 1 : 0) * Lay::KB, p.k, p.ks, p.kp);
             if (tid < 48)
                 cp16(sm0 + Lay::oVec + (i & 1) * 768 + tid * 16,
-                     p.vec + ((slot0 + c) * p.H + h) * 3 * kDeltaC + tid * 4, true);
+                     p.vec + ((slot0 + c) * p.H + h) * kDeltaVec + tid * 4, true);
         };
         auto load_vt = [&](int c) {
             const long long sh = (slot0 + c) * p.H + h;
