@@ -500,8 +500,8 @@ int block_norm_fwd(const void *x, const void *z, const void *r, const float *s,
  * dw_pre, db_pre (D): each in a fixed order, the same bits on every call.
  * With no rows the sums are zero.  dr may be dr_out, and dx may be x if x is
  * contiguous; otherwise no output may overlap an input or another output.
- * Scratch for the partial sums (8880 * D bytes at most) comes from the
- * stream-ordered pool. */
+ * Scratch for the partial sums (8880 * D bytes at most, none for a few rows)
+ * comes from the stream-ordered pool. */
 int block_norm_bwd(const void *x, const void *z, const void *r_out, const float *s,
                    const float *w_post, const float *b_post, const float *w_pre,
                    const void *dr_out, const void *dy, void *dx, void *dz, void *dr, float *ds,

@@ -11,6 +11,8 @@
 namespace {
 
 constexpr int kNormMaxD = 8192;
+// the backward in one cluster: its CTAs, rows to a team, and columns whose sums fit beside the teams' in 48 KB
+constexpr int kClusterCtas = 8, kClusterRows = 2, kClusterD = 1536;
 
 struct NormCall {
     ss2d::NormParams p;
@@ -232,20 +234,33 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
     if (!z)
         p.dz = nullptr;
     const ss2d::NormPlan pl = norm_plan(c, true);
-    const int threads = p.tpr > 256 ? p.tpr : 256;
-    const long long teams = threads / p.tpr, ctas = (rows + teams - 1) / teams;
+    int threads = p.tpr > 256 ? p.tpr : 256;
+    auto count = [&](int n) { return (rows + n / p.tpr - 1) / (n / p.tpr); };   // CTAs of n threads, a row to a team
     // CTAs that the kernel's registers let onto an SM; more of them only add partials
     const int fill = 148 * (pl.M == ss2d::kNormAny ? 2 : ss2d::norm_bwd_ctas(pl.E));
-    const int grid = ctas > fill ? fill : (int)ctas;
+    int grid = (int)(count(threads) < fill ? count(threads) : fill);
+    // Few rows: one cluster of up to eight CTAs, which adds up its CTAs' sums in their shared memory; no scratch and
+    // no second launch.  With a row to a team (16 of 191 float32 values: 10.2 -> 9.0 us) the device gains too; up to
+    // two rows, in CTAs of 512 threads where the kernel has them, only the host does (197 rows: 9.9 -> 13.2 us in a
+    // graph, but a call from Python 25.6 -> 20.3); with four rows the device took 18.7 us.
+    if (p.cols && p.D <= kClusterD && grid > kClusterCtas && pl.M == ss2d::kNormAny)
+        threads = 512;
+    const bool cluster = p.cols && p.D <= kClusterD && count(threads) <= kClusterCtas * kClusterRows;
+    if (cluster)
+        grid = (int)(count(threads) < kClusterCtas ? count(threads) : kClusterCtas);
+    else if (p.tpr <= 256)
+        threads = 256;
+    for (int i = 0; i < ss2d::kNormCols; ++i)
+        p.sums[i] = out.out[i];
     void *part = nullptr;
-    if (p.cols) {
+    if (p.cols && !cluster) {
         rc = ss2d::scratch_alloc(&part, sizeof(float) * ss2d::kNormCols * grid * (size_t)D, st);
         if (rc != SS2D_OK)
             return rc;
     }
     p.part = static_cast<float *>(part);
     e = launch_norm(c, pl, true, grid, threads, st);
-    if (e == cudaSuccess && p.cols) {
+    if (e == cudaSuccess && part) {
         e = ss2d::launch_norm_colsum(p.part, out, grid, D, st);
     }
     cudaError_t ef = cudaSuccess;

@@ -48,7 +48,8 @@ struct NormParams {
     void *r_out, *y;                  // forward
     const void *dr_out, *dy;          // backward
     void *dx, *dz, *dr;
-    float *part;                      // [kNormCols][gridDim.x][D] partial column sums
+    float *part;                      // [kNormCols][gridDim.x][D] partial column sums (null: the grid is one cluster)
+    float *sums[kNormCols];           // column sums that a cluster writes itself
     int cols;                         // bit c: column sum c is wanted
     long long rows, xs, zs;           // row i of x starts at (i / group) * xs + (i % group) * D
     int group;
@@ -538,6 +539,21 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p)
     }
 }
 
+// Every CTA of the cluster is here, what they wrote to shared memory can be read; a float of CTA `rank`
+__device__ __forceinline__ void norm_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float norm_cluster_read(const float *v, unsigned rank)
+{
+    float f;
+    asm volatile("{\n.reg .u32 a;\nmapa.shared::cluster.u32 a, %1, %2;\nld.shared::cluster.f32 %0, [a];\n}"
+                 : "=f"(f)
+                 : "r"((unsigned)__cvta_generic_to_shared(v)), "r"(rank)
+                 : "memory");
+    return f;
+}
+
 // CTAs of 256 threads per SM of the compiled combinations
 __host__ __device__ constexpr int norm_bwd_ctas(int E) { return E == 8 ? 3 : 2; }
 
@@ -745,7 +761,8 @@ __global__ void __launch_bounds__(M == kNormAny ? 512 : 256, M == kNormAny ? 1 :
             if (live && on(i))
                 norm_store<Tin, V>(static_cast<Tin *>(p.dx) + o * D, col(i), g + i * V);
     }
-    // the CTA's column sums, its teams in order
+    // the CTA's column sums, its teams in order; a cluster keeps them in shared memory behind csum
+    float *mine = csum + blockDim.x * E;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         if (!(p.cols >> c & 1))
@@ -763,8 +780,24 @@ __global__ void __launch_bounds__(M == kNormAny ? 512 : 256, M == kNormAny ? 1 :
             float v = 0.f;
             for (int t = 0; t < teams; ++t)
                 v += csum[(t * E + e) * p.tpr + l];
-            p.part[((size_t)c * gridDim.x + blockIdx.x) * D + d] = v;
+            if (p.part)
+                p.part[((size_t)c * gridDim.x + blockIdx.x) * D + d] = v;
+            else
+                mine[c * D + d] = v;
         }
+    }
+    if (p.cols && !p.part) {
+        norm_cluster_sync();
+        for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < NC * D; i += gridDim.x * blockDim.x) {
+            const int c = i / D;
+            if (!(p.cols >> c & 1))
+                continue;
+            float v = 0.f;
+            for (unsigned r = 0; r < gridDim.x; ++r)
+                v += norm_cluster_read(mine + i, r);
+            p.sums[c][i - c * D] = v;
+        }
+        norm_cluster_sync();   // no CTA leaves while its sums are read
     }
 }
 

@@ -12,15 +12,24 @@ cudaError_t launch_norm_parts(const NormParams &p, bool bwd, int grid, int threa
         norm_fwd_kernel<Tin, Tr, V, E, M><<<grid, threads, 0, st>>>(p);
         return cudaGetLastError();
     }
-    const size_t smem = sizeof(float) * threads * E;
-    if constexpr (M == kNormAny || (M & kHasBias)) {
-        if (p.cols >> 3) {
-            norm_bwd_kernel<Tin, Tr, V, E, true, M><<<grid, threads, smem, st>>>(p);
-            return cudaGetLastError();
-        }
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {(unsigned)grid, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = sizeof(float) * threads * E;
+    cfg.stream = st;
+    if (p.cols && !p.part) {   // one cluster, which sums its CTAs' columns
+        cfg.dynamicSmemBytes += sizeof(float) * kNormCols * p.D;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
     }
-    norm_bwd_kernel<Tin, Tr, V, E, false, M><<<grid, threads, smem, st>>>(p);
-    return cudaGetLastError();
+    if constexpr (M == kNormAny || (M & kHasBias)) {
+        if (p.cols >> 3)
+            return cudaLaunchKernelEx(&cfg, norm_bwd_kernel<Tin, Tr, V, E, true, M>, p);
+    }
+    return cudaLaunchKernelEx(&cfg, norm_bwd_kernel<Tin, Tr, V, E, false, M>, p);
 }
 template <typename Tin, typename Tr, int V, int E>
 cudaError_t launch_norm_full(const NormParams &p, int M, bool bwd, int grid, int threads, cudaStream_t st)

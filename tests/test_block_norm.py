@@ -267,6 +267,15 @@ def check(a, dtype, rdt, seed=1):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,D,post,pre", [(64, 191, "rms", "none"), (256, 191, "layer", "rms"), (257, 191, "rms", "none"),
+                                             (512, 64, "rms", "none"), (513, 64, "none", "layer"), (16, 1536, "rms", "layer"),
+                                             (33, 1536, "rms", "none"), (5, 1544, "layer", "layer")])
+def test_column_sums_on_both_sides_of_one_cluster(rows, D, post, pre):
+    for bias in (False, True):
+        check(make(rows, D, post, pre, gate=True, res=pre != "none", scale=pre != "none", bias=bias), "bf16", "bf16")
+
+
+@pytest.mark.gpu
 def test_many_rows_and_repeatable_sums():
     a = make(5003, 200)
     check(a, "bf16", "f32")
