@@ -126,7 +126,9 @@ int run_chunked(Call &c, bool bwd)
     const size_t segs = !p.SC ? 0 : p.cu ? p.nslots / p.SC + p.nseq
                                          : (size_t)p.nseq * ((p.NC + p.SC - 1) / p.SC);
     const size_t n = (size_t)p.nslots, nh = n * p.H, part = ss2d::kTriBytes;
-    const size_t kp = pl.npi > 1 ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
+    // the chains of float16 read k and q as they are, but for the form of few wide heads
+    const bool parts = c.dtype == SS2D_F32 || (c.dtype == SS2D_F16 && pl.dkp == 128 && (p.SC || !ss2d::delta_wide(p, bwd)));
+    const size_t kp = parts ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
     const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
     const size_t ns = segs * p.H * p.DV * pl.dkp * 4;
     const size_t size[] = {kp, kp, nh * pl.np * part, nh * pl.npp * part, nh * ss2d::kDeltaVec * 4, sx, sx, vx, vx, ns, ns, bwd ? ns : 0, bwd ? ns : 0,
@@ -142,8 +144,8 @@ int run_chunked(Call &c, bool bwd)
         return rc;
     char *b = static_cast<char *>(scratch);
     auto f = [&](int i) { return reinterpret_cast<float *>(b + off[i]); };
-    p.kp = b + off[0];
-    p.qp = b + off[1];
+    p.kp = parts ? b + off[0] : nullptr;
+    p.qp = parts ? b + off[1] : nullptr;
     p.Tp = b + off[2];
     p.Pp = b + off[3];
     p.vec = f(4);

@@ -63,7 +63,7 @@ struct DeltaParams {
     // scratch of the chunks
     int NC;                        // chunk slots per sequence (cu null)
     long long nslots;
-    void *kp, *qp;                 // bf16 parts of k and q per (slot, key head): [NPI][64][DKP]
+    void *kp, *qp;                 // bf16 parts of k and q per (slot, key head): [NPI][64][DKP]; null: nobody reads them
     void *Tp, *Pp;                 // bf16 parts of T and P per (slot, head), packed blocks
     float *vec;                    // per (slot, head): e^c, e^{c_last - c}, beta, c log2(e) and what it lacks (64 each)
     // segments of a long chain: SC chunks each (0: none)
@@ -328,16 +328,21 @@ __device__ __forceinline__ void mma_parts(float (&c0)[4], float (&c1)[4], const 
 }
 
 // B from rows of a [n][k] tile: B element (k, n) is row n, column k
+template <int RB, int N>
+__device__ __forceinline__ void frag_rows(uint32_t tile, int part, int row, int piece, uint32_t (&b)[N][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+        ldsm4(tile + m * part + swz<RB>(row + (lane & 7) + (lane >> 4) * 8, piece + (lane >> 3 & 1)), b[m]);
+}
 template <int RB, int NA, int NB, int KEEP>
 __device__ __forceinline__ void mma_rows(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], uint32_t tile,
                                          int part, int row, int piece)
 {
     constexpr int NL = NB < KEEP ? NB : KEEP;
-    const int lane = threadIdx.x & 31;
     uint32_t b[NL][4];
-#pragma unroll
-    for (int m = 0; m < NL; ++m)
-        ldsm4(tile + m * part + swz<RB>(row + (lane & 7) + (lane >> 4) * 8, piece + (lane >> 3 & 1)), b[m]);
+    frag_rows<RB, NL>(tile, part, row, piece, b);
     mma_parts<NA, NL, KEEP>(c0, c1, a, b);
 }
 // B from a [k][n] tile: rows k, columns n
@@ -357,6 +362,77 @@ __device__ __forceinline__ void mma_cols(float (&c0)[4], float (&c1)[4], const u
     uint32_t b[NL][4];
     frag_cols<RB, NL>(tile, part, row, piece, b);
     mma_parts<NA, NL, KEEP>(c0, c1, a, b);
+}
+
+// ---- float16 inputs as they are -----------------------------------------------
+// K and Q of float16 calls are one exact float16 operand each, where bfloat16 parts would
+// be two; what multiplies them is split into two float16 parts (22 bits) after
+// scaling by the power of two that brings the warp's largest value into 2^13 .. 2^14: two
+// products instead of five, and half the shared memory.  A value smaller than the largest
+// by 2^16 and more keeps fewer bits, but none is off by more than 2^-38 of the largest.
+struct HalfScale {
+    float up, down;
+};
+template <int N>
+__device__ __forceinline__ HalfScale half_scale(const float (&v)[N][4])
+{
+    float m = 0.f;   // a NaN is passed over here and stays one in its part
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            m = fmaxf(m, fabsf(v[n][j]));
+    const uint32_t e = max(__reduce_max_sync(0xffffffffu, __float_as_uint(m)) >> 23, 14u);
+    return {__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
+}
+__device__ __forceinline__ void half_split(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+__device__ __forceinline__ void half_frag(const float (&c0)[4], const float (&c1)[4], float up, uint32_t (&a)[2][4])
+{
+    half_split(c0[0] * up, c0[1] * up, a[0][0], a[1][0]);
+    half_split(c0[2] * up, c0[3] * up, a[0][1], a[1][1]);
+    half_split(c1[0] * up, c1[1] * up, a[0][2], a[1][2]);
+    half_split(c1[2] * up, c1[3] * up, a[0][3], a[1][3]);
+}
+__device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c0, c1 += A B: FROM0 summed from zero and joined by a rounding addition that takes the scale off (see mma_parts),
+// otherwise in the scaled sum itself
+template <bool FROM0>
+__device__ __forceinline__ void mma_half(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[2][4],
+                                         const uint32_t (&b)[4], float down)
+{
+    if constexpr (FROM0) {
+        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = 1; n >= 0; --n) {
+            mma16816h(d0, a[n], b[0], b[1]);
+            mma16816h(d1, a[n], b[2], b[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c0[j] = fmaf(d0[j], down, c0[j]);
+            c1[j] = fmaf(d1[j], down, c1[j]);
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            mma16816h(c0, a[n], b[0], b[1]);
+            mma16816h(c1, a[n], b[2], b[3]);
+        }
+    }
 }
 
 // B from a 16 x 16 block of packed parts: its rows are n (columns k), or its rows are k (columns n)
@@ -726,7 +802,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
         delta_decays(p, q, t0, hk * G, ch, cl, be);
     cp_wait();
     __syncthreads();
-    if (NPI > 1) {   // scratch copies, rows in order (not swizzled)
+    if (NPI > 1 && p.kp) {   // scratch copies, rows in order (not swizzled)
         const long long base = ((long long)blockIdx.x * p.HK + hk) * NPI * PB;
         for (int i = tid; i < NPI * kDeltaC * (DKP / 8); i += kPrepThreads) {
             const int r = i / (DKP / 8), pc = i % (DKP / 8);   // r counts the parts' rows

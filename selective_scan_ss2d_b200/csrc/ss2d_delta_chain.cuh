@@ -35,8 +35,10 @@ enum { kChainOut = 0, kChainState = 1, kChainRev = 2 };
 template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP, int STAGES>
 struct ChainLayout {
     static constexpr int NPI = DeltaParts<Tin>::n;
+    static constexpr bool HALF = std::is_same_v<Tin, __half>;    // K and Q as they are
+    static constexpr int NKQ = HALF ? 1 : NPI;                   // their parts
     static constexpr int DVT = NW * 16;
-    static constexpr int KB = NPI * kDeltaC * DKP * 2;           // K; Q the same
+    static constexpr int KB = NKQ * kDeltaC * DKP * 2;           // K; Q the same
     static constexpr int VRB = sizeof(Tin) == 2 ? DVT * 2 : (DVT + 4) * 4;   // row of V or dO
     static constexpr int oK = 0;
     static constexpr int oQ = KB;
@@ -58,7 +60,8 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                                             bool every = false)
 {
     using Lay = ChainLayout<Tin, DKP, NW, MODE, NP, NPP, STAGES>;
-    constexpr int NPI = Lay::NPI, NT = NW * 32, RBK = DKP * 2, PBK = kDeltaC * RBK, NK = DKP / 8;
+    constexpr bool HALF = Lay::HALF;
+    constexpr int NPI = Lay::NPI, NKQ = Lay::NKQ, NT = NW * 32, RBK = DKP * 2, PBK = kDeltaC * RBK, NK = DKP / 8;
     extern __shared__ __align__(128) unsigned char dsm[];
     const uint32_t sm0 = smem_addr(dsm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,12 +102,12 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
             const uint32_t base = sm0 + st * Lay::stage;
             const long long slot = slot0 + c, sh = slot * p.H + h;
             const int t0 = c * kDeltaC;
-            for (int i = tid; i < NPI * kDeltaC * (DKP / 8); i += NT) {
+            for (int i = tid; i < NKQ * kDeltaC * (DKP / 8); i += NT) {
                 const int r = i / (DKP / 8), pc = i % (DKP / 8);   // r counts the parts' rows
                 const uint32_t dst = base + (r / kDeltaC) * PBK + swz<RBK>(r % kDeltaC, pc);
                 const char *ks, *qs;
                 bool on = true;
-                if constexpr (NPI == 1) {
+                if constexpr (NKQ == 1) {
                     on = t0 + r < q.len && pc * 8 < p.DK;
                     const long long tok = delta_token(p, q, on ? t0 + r : 0);
                     const long long col = (long long)hk * p.DK + (on ? pc * 8 : 0);
@@ -261,14 +264,36 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                     for (int j = 0; j < 4; ++j)
                         R[n][j] = O[n][j] = 0.f;
                 // (K S)^T
+                HalfScale hs;
+                if constexpr (HALF)
+                    hs = half_scale(S);
 #pragma unroll
                 for (int ks = 0; ks < DKP / 16; ++ks) {
-                    uint32_t a[NP][4];
-                    frag_a<NP>(S[2 * ks], S[2 * ks + 1], a);
+                    if constexpr (HALF) {
+                        uint32_t a[2][4], kb[1][4];
+                        half_frag(S[2 * ks], S[2 * ks + 1], hs.up, a);
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (b < NB)
-                            mma_rows<RBK, NP, NPI, NP>(R[2 * b], R[2 * b + 1], a, sa + Lay::oK, PBK, b * 16, ks * 2);
+                        for (int b = 0; b < 4; ++b)
+                            if (b < NB) {
+                                frag_rows<RBK, 1>(sa + Lay::oK, PBK, b * 16, ks * 2, kb);
+                                mma_half<NP == 3>(R[2 * b], R[2 * b + 1], a, kb[0], hs.down);
+                            }
+                    } else {
+                        uint32_t a[NP][4];
+                        frag_a<NP>(S[2 * ks], S[2 * ks + 1], a);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b < NB)
+                                mma_rows<RBK, NP, NPI, NP>(R[2 * b], R[2 * b + 1], a, sa + Lay::oK, PBK, b * 16,
+                                                           ks * 2);
+                    }
+                }
+                if constexpr (HALF && NP != 3) {
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            R[n][j] *= hs.down;
                 }
                 if constexpr (MODE != kChainRev) {
 #pragma unroll
@@ -312,19 +337,31 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                         // O^T = scale e^c (Q S)^T + V'^T P^T
 #pragma unroll
                         for (int ks = 0; ks < DKP / 16; ++ks) {
-                            uint32_t a[NPP][4];
-                            frag_a<NPP>(S[2 * ks], S[2 * ks + 1], a);
+                            if constexpr (HALF) {
+                                uint32_t a[2][4], qb[1][4];
+                                half_frag(S[2 * ks], S[2 * ks + 1], hs.up, a);
 #pragma unroll
-                            for (int b = 0; b < 4; ++b)
-                                if (b < NB)
-                                    mma_rows<RBK, NPP, NPI, NPP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oQ, PBK, b * 16,
-                                                                 ks * 2);
+                                for (int b = 0; b < 4; ++b)
+                                    if (b < NB) {
+                                        frag_rows<RBK, 1>(sa + Lay::oQ, PBK, b * 16, ks * 2, qb);
+                                        mma_half<false>(O[2 * b], O[2 * b + 1], a, qb[0], hs.down);
+                                    }
+                            } else {
+                                uint32_t a[NPP][4];
+                                frag_a<NPP>(S[2 * ks], S[2 * ks + 1], a);
+#pragma unroll
+                                for (int b = 0; b < 4; ++b)
+                                    if (b < NB)
+                                        mma_rows<RBK, NPP, NPI, NPP>(O[2 * b], O[2 * b + 1], a, sa + Lay::oQ, PBK,
+                                                                     b * 16, ks * 2);
+                            }
                         }
+                        const float os = HALF ? p.scale * hs.down : p.scale;
 #pragma unroll
                         for (int n = 0; n < 8; ++n)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                O[n][j] *= p.scale * eg[n * 8 + t2 + (j & 1)];
+                                O[n][j] *= os * eg[n * 8 + t2 + (j & 1)];
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
                             if (ks >= NB)
@@ -399,15 +436,31 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         S[n][j] *= elast;
+                if constexpr (HALF)
+                    hs = half_scale(R);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     if (ks >= NB)
                         continue;
-                    uint32_t a[NP][4];
-                    frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
+                    // S^T += A B in two float16 parts of A
+                    auto half_cols = [&](const float (&c0)[4], const float (&c1)[4], const HalfScale &h, int at) {
+                        uint32_t a[2][4], kb[1][4];
+                        half_frag(c0, c1, h.up, a);
 #pragma unroll
-                    for (int nt = 0; nt < NK; nt += 2)
-                        mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oK, PBK, ks * 16, nt);
+                        for (int nt = 0; nt < NK; nt += 2) {
+                            frag_cols<RBK, 1>(sa + at, PBK, ks * 16, nt, kb);
+                            mma_half<true>(S[nt], S[nt + 1], a, kb[0], h.down);
+                        }
+                    };
+                    uint32_t a[NP][4];
+                    if constexpr (HALF) {
+                        half_cols(R[2 * ks], R[2 * ks + 1], hs, Lay::oK);
+                    } else {
+                        frag_a<NP>(R[2 * ks], R[2 * ks + 1], a);
+#pragma unroll
+                        for (int nt = 0; nt < NK; nt += 2)
+                            mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oK, PBK, ks * 16, nt);
+                    }
                     if constexpr (MODE == kChainRev) {
                         float v[2][4];
                         values(sb, ks, v[0], v[1]);
@@ -416,10 +469,14 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 v[e][j] *= p.scale * eg[ks * 16 + e * 8 + t2 + (j & 1)];
-                        frag_a<NP>(v[0], v[1], a);
+                        if constexpr (HALF) {
+                            half_cols(v[0], v[1], half_scale(v), Lay::oQ);
+                        } else {
+                            frag_a<NP>(v[0], v[1], a);
 #pragma unroll
-                        for (int nt = 0; nt < NK; nt += 2)
-                            mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, nt);
+                            for (int nt = 0; nt < NK; nt += 2)
+                                mma_cols<RBK, NP, NPI, NP>(S[nt], S[nt + 1], a, sa + Lay::oQ, PBK, ks * 16, nt);
+                        }
                     }
                 }
             };

@@ -28,17 +28,6 @@ cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// CTAs of 64 columns of DV above which a chain counts as many (two to an SM)
-constexpr long long kWideCtas = 2 * 148;
-
-// chains of a pass: segments (every slot that may hold one), or sequences
-inline long long delta_units(const DeltaParams &p)
-{
-    if (!p.SC)
-        return p.nseq;
-    return p.cu ? p.nslots / p.SC + p.nseq : (long long)p.nseq * ((p.NC + p.SC - 1) / p.SC);
-}
-
 inline dim3 chain_grid(const DeltaParams &p, int tiles)
 {
     const long long units = delta_units(p);
@@ -163,8 +152,7 @@ cudaError_t launch_segments(const DeltaParams &p, cudaStream_t st)
 template <typename Tin, int DKP, int NP, int NPP>
 cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
 {
-    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p);
-    if (ctas > kWideCtas)
+    if (delta_wide(p, false))
         return launch_wide_out<Tin, DKP, NP, NPP, 1>(p, st);
     if constexpr (chain_split<Tin, DKP>())
         return launch_split_out<Tin, DKP, NP, NPP>(p, st);
@@ -177,8 +165,7 @@ cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
 template <typename Tin, int DKP>
 cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
 {
-    const long long ctas = (long long)((p.DV + 63) / 64) * p.H * delta_units(p);
-    if (ctas * 2 > kWideCtas) {
+    if (delta_wide(p, true)) {
         const cudaError_t e = launch_wide_one<Tin, DKP, kChainState>(p, st);
         return e != cudaSuccess ? e : launch_wide_one<Tin, DKP, kChainRev>(p, st);
     }

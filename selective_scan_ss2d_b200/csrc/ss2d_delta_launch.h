@@ -24,4 +24,19 @@ cudaError_t launch_delta_bwd_bf16(const DeltaParams &p, const DeltaPlan &pl, cud
 cudaError_t launch_delta_bwd_f16(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st);
 cudaError_t launch_delta_bwd_f32(const DeltaParams &p, const DeltaPlan &pl, cudaStream_t st);
 
+// CTAs of 64 columns of DV above which a chain counts as many (two to an SM)
+constexpr long long kWideCtas = 2 * 148;
+
+// chains of a pass: segments (every slot that may hold one), or sequences
+inline long long delta_units(const DeltaParams &p)
+{
+    if (!p.SC)
+        return p.nseq;
+    return p.cu ? p.nslots / p.SC + p.nseq : (long long)p.nseq * ((p.NC + p.SC - 1) / p.SC);
+}
+inline bool delta_wide(const DeltaParams &p, bool bwd)
+{
+    return (long long)((p.DV + 63) / 64) * p.H * delta_units(p) * (bwd ? 2 : 1) > kWideCtas;
+}
+
 }  // namespace ss2d
