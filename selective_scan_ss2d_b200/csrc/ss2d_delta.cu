@@ -126,8 +126,9 @@ int run_chunked(Call &c, bool bwd)
     const size_t segs = !p.SC ? 0 : p.cu ? p.nslots / p.SC + p.nseq
                                          : (size_t)p.nseq * ((p.NC + p.SC - 1) / p.SC);
     const size_t n = (size_t)p.nslots, nh = n * p.H, part = ss2d::kTriBytes;
-    // the chains of float16 read k and q as they are, but for the form of few wide heads
-    const bool parts = c.dtype == SS2D_F32 || (c.dtype == SS2D_F16 && pl.dkp == 128 && (p.SC || !ss2d::delta_wide(p, bwd)));
+    // float16 chains read k and q as they are, but for the outputs of few wide heads
+    const bool parts = c.dtype == SS2D_F32 ||
+                       (c.dtype == SS2D_F16 && !bwd && pl.dkp == 128 && ss2d::delta_split_f16(p));
     const size_t kp = parts ? n * p.HK * pl.npi * kDeltaC * pl.dkp * 2 : 0;
     const size_t sx = bwd ? nh * p.DV * pl.dkp * 4 : 0, vx = bwd ? nh * p.DV * kDeltaC * 4 : 0;
     const size_t ns = segs * p.H * p.DV * pl.dkp * 4;

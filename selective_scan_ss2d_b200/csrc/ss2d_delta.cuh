@@ -719,7 +719,7 @@ __device__ __forceinline__ void delta_stage_parts(const DeltaParams &p, const vo
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
 // acc (16 rows x 8 NT columns of a warp) += rows r0.. of tile A times rows n0.. of tile B, transposed: sums over DKP
-template <int DKP, int NPI, int NT>
+template <int DKP, int NPI, int NT, bool HALF = false>
 __device__ __forceinline__ void delta_rows_product(uint32_t A, uint32_t B, int r0, int n0, float (&acc)[NT][4])
 {
     constexpr int RB = DKP * 2, PB = kDeltaC * RB;
@@ -737,7 +737,12 @@ __device__ __forceinline__ void delta_rows_product(uint32_t A, uint32_t B, int r
             for (int m = 0; m < NPI; ++m)
                 ldsm4(B + m * PB + swz<RB>(n0 + nt * 8 + (lane & 7) + (lane >> 4) * 8, ks * 2 + (lane >> 3 & 1)),
                       b[m]);
-            mma_parts<NPI, NPI, 3>(acc[nt], acc[nt + 1], a, b);
+            if constexpr (HALF) {   // float16 as it is
+                mma16816h(acc[nt], a[0], b[0][0], b[0][1]);
+                mma16816h(acc[nt + 1], a[0], b[0][2], b[0][3]);
+            } else {
+                mma_parts<NPI, NPI, 3>(acc[nt], acc[nt + 1], a, b);
+            }
         }
     }
 }
@@ -781,12 +786,13 @@ __device__ __forceinline__ void delta_decays(const DeltaParams &p, const DeltaSe
     be[2 * lane + 1] = b[1];
 }
 
-// NPT parts of T, NPP of P are written
-template <typename Tin, int DKP, int NPT, int NPP>
+// NPT parts of T, NPP of P are written; PARTS: k and q are split into bf16 parts, and copied where they are read as such
+template <typename Tin, int DKP, int NPT, int NPP, bool PARTS>
 __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const DeltaParams p)
 {
-    using Lay = PrepLayout<DKP, DeltaParts<Tin>::n, NPT, NPP>;
-    constexpr int NPI = DeltaParts<Tin>::n, RB = DKP * 2, PB = kDeltaC * RB;
+    constexpr int NPI = PARTS ? DeltaParts<Tin>::n : 1, RB = DKP * 2, PB = kDeltaC * RB;
+    constexpr bool HALF = !PARTS && std::is_same_v<Tin, __half>;
+    using Lay = PrepLayout<DKP, NPI, NPT, NPP>;
     extern __shared__ __align__(128) unsigned char dsm[];
     __shared__ float ch[kDeltaC], cl[kDeltaC], be[kDeltaC];
     int s, c;
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
         delta_decays(p, q, t0, hk * G, ch, cl, be);
     cp_wait();
     __syncthreads();
-    if (NPI > 1 && p.kp) {   // scratch copies, rows in order (not swizzled)
+    if constexpr (PARTS) {   // scratch copies, rows in order (not swizzled)
         const long long base = ((long long)blockIdx.x * p.HK + hk) * NPI * PB;
         for (int i = tid; i < NPI * kDeltaC * (DKP / 8); i += kPrepThreads) {
             const int r = i / (DKP / 8), pc = i % (DKP / 8);   // r counts the parts' rows
@@ -826,8 +832,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const Delta
         for (int j = 0; j < 4; ++j)
             kk[n][0][j] = kk[n][1][j] = qk[n][0][j] = qk[n][1][j] = 0.f;
         if (n < nblk) {
-            delta_rows_product<DKP, NPI, 2>(smem_addr(kt), smem_addr(kt), bi(n) * 16, bj(n) * 16, kk[n]);
-            delta_rows_product<DKP, NPI, 2>(smem_addr(qt), smem_addr(kt), bi(n) * 16, bj(n) * 16, qk[n]);
+            delta_rows_product<DKP, NPI, 2, HALF>(smem_addr(kt), smem_addr(kt), bi(n) * 16, bj(n) * 16, kk[n]);
+            delta_rows_product<DKP, NPI, 2, HALF>(smem_addr(qt), smem_addr(kt), bi(n) * 16, bj(n) * 16, qk[n]);
         }
     }
     const uint32_t sA = smem_addr(dsm), sX = sA + Lay::oT;

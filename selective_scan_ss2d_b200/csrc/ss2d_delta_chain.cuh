@@ -264,7 +264,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                     for (int j = 0; j < 4; ++j)
                         R[n][j] = O[n][j] = 0.f;
                 // (K S)^T
-                HalfScale hs;
+                [[maybe_unused]] HalfScale hs{1.f, 1.f};
                 if constexpr (HALF)
                     hs = half_scale(S);
 #pragma unroll
@@ -452,7 +452,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                             mma_half<true>(S[nt], S[nt + 1], a, kb[0], h.down);
                         }
                     };
-                    uint32_t a[NP][4];
+                    [[maybe_unused]] uint32_t a[NP][4];
                     if constexpr (HALF) {
                         half_cols(R[2 * ks], R[2 * ks + 1], hs, Lay::oK);
                     } else {

@@ -16,11 +16,24 @@ cudaError_t delta_smem(void (*kern)(A...), int bytes)
                              : cudaSuccess;
 }
 
-template <typename Tin, int DKP, int NPT, int NPP>
-cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
+// Which form a chain takes.  Many chains (more than kWideCtas CTAs): one warp to 16
+// columns, one stage, two or three CTAs per SM.  Few: one warp with two stages for
+// heads of up to 64 in 16 bits (4.4 us a chunk against 5.1 with four warps), four warps for
+// wider heads and float32 (both chains of 4096 tokens, 128 x 128: 533 us against 621; seven
+// float32 sequences of 32 x 64: 67 against 100).  float16, whose one-warp form has fewer products,
+// takes four warps only for the outputs of few wide heads (4096 tokens, 32 chains: 389 us a call against
+// 488; 500 tokens, 128 chains 151 against 131; a backward pass of 32 chains 1298 against 1118,
+// segments 291 against 237).
+template <typename Tin, int DKP>
+constexpr bool chain_split_out() { return sizeof(Tin) == 4 || DKP == 128; }
+template <typename Tin, int DKP>
+constexpr bool chain_split() { return sizeof(Tin) == 4 || (DKP == 128 && !std::is_same_v<Tin, __half>); }
+
+template <typename Tin, int DKP, int NPT, int NPP, bool PARTS>
+cudaError_t launch_prep_as(const DeltaParams &p, cudaStream_t st)
 {
-    constexpr int smem = PrepLayout<DKP, DeltaParts<Tin>::n, NPT, NPP>::bytes;
-    auto kern = delta_prep_kernel<Tin, DKP, NPT, NPP>;
+    constexpr int smem = PrepLayout<DKP, PARTS ? DeltaParts<Tin>::n : 1, NPT, NPP>::bytes;
+    auto kern = delta_prep_kernel<Tin, DKP, NPT, NPP, PARTS>;
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
@@ -32,6 +45,18 @@ inline dim3 chain_grid(const DeltaParams &p, int tiles)
 {
     const long long units = delta_units(p);
     return dim3(tiles, p.H, (unsigned)(units < 65535 ? units : 65535));
+}
+
+// p.kp: the chain reads k and q in bf16 parts
+template <typename Tin, int DKP, int NPT, int NPP>
+cudaError_t launch_prep(const DeltaParams &p, cudaStream_t st)
+{
+    if constexpr (sizeof(Tin) == 4)
+        return launch_prep_as<Tin, DKP, NPT, NPP, true>(p, st);
+    else if constexpr (chain_split_out<Tin, DKP>() && std::is_same_v<Tin, __half> && NPP == 2)
+        return p.kp ? launch_prep_as<Tin, DKP, NPT, NPP, true>(p, st) : launch_prep_as<Tin, DKP, NPT, NPP, false>(p, st);
+    else
+        return launch_prep_as<Tin, DKP, NPT, NPP, false>(p, st);
 }
 
 // ---- one warp to 16 columns of DV, CTAs of 64 columns
@@ -70,19 +95,24 @@ cudaError_t launch_wide_both(const DeltaParams &p, cudaStream_t st)
 }
 
 // ---- four warps to 16 columns: four groups to a CTA and two buffers of K where they fit
-template <typename Tin, int DKP, int MODE, int NP, int NPP>
+template <typename Tin, int DKP, int MODE, int NP, int NPP, int MOST = 4>
 struct SplitShape {
     static constexpr int most = 226 * 1024;
-    static constexpr int groups = SplitLayout<Tin, DKP, 4, MODE, NP, NPP, 2>::bytes <= most ? 4 : 2;
+    static constexpr int groups = SplitLayout<Tin, DKP, 4, MODE, NP, NPP, 2>::bytes <= most ? MOST : 2;
     static constexpr int kbuf = SplitLayout<Tin, DKP, groups, MODE, NP, NPP, 2>::bytes <= most ? 2 : 1;
     static constexpr int bytes = SplitLayout<Tin, DKP, groups, MODE, NP, NPP, kbuf>::bytes;
     static_assert(bytes <= most, "shared memory");
     static int tiles(int n) { return (n + groups * 16 - 1) / (groups * 16); }
 };
-template <typename Tin, int DKP, int NP, int NPP>
+template <typename Tin, int DKP, int NP, int NPP, int MOST = 4>
 cudaError_t launch_split_out(const DeltaParams &p, cudaStream_t st)
 {
-    using Sh = SplitShape<Tin, DKP, kChainOut, NP, NPP>;
+    using Sh = SplitShape<Tin, DKP, kChainOut, NP, NPP, MOST>;
+    // two groups to a CTA while each has an SM (bfloat16, 4096 tokens, 32 chains of 128 x 128: 467 -> 313 us a call)
+    if constexpr (MOST == 4 && Sh::groups == 4) {
+        if (2 * (long long)Sh::tiles(p.DV) * p.H * delta_units(p) <= 148)
+            return launch_split_out<Tin, DKP, NP, NPP, 2>(p, st);
+    }
     auto kern = delta_split_out_kernel<Tin, DKP, Sh::groups, NP, NPP, Sh::kbuf>;
     const cudaError_t e = delta_smem(kern, Sh::bytes);
     if (e != cudaSuccess)
@@ -90,10 +120,14 @@ cudaError_t launch_split_out(const DeltaParams &p, cudaStream_t st)
     kern<<<chain_grid(p, Sh::tiles(p.DV)), Sh::groups * 128, Sh::bytes, st>>>(p, delta_units(p));
     return cudaGetLastError();
 }
-template <typename Tin, int DKP>
+template <typename Tin, int DKP, int MOST = 4>
 cudaError_t launch_split_both(const DeltaParams &p, cudaStream_t st)
 {
-    using Sh = SplitShape<Tin, DKP, kChainRev, 3, 3>;   // the larger of the two
+    using Sh = SplitShape<Tin, DKP, kChainRev, 3, 3, MOST>;   // the larger of the two
+    if constexpr (MOST == 4 && Sh::groups == 4) {
+        if (4 * (long long)Sh::tiles(p.DV) * p.H * delta_units(p) <= 148)
+            return launch_split_both<Tin, DKP, 2>(p, st);
+    }
     auto kern = delta_split_both_kernel<Tin, DKP, Sh::groups, Sh::kbuf>;
     const cudaError_t e = delta_smem(kern, Sh::bytes);
     if (e != cudaSuccess)
@@ -101,14 +135,6 @@ cudaError_t launch_split_both(const DeltaParams &p, cudaStream_t st)
     kern<<<chain_grid(p, 2 * Sh::tiles(p.DV)), Sh::groups * 128, Sh::bytes, st>>>(p, delta_units(p));
     return cudaGetLastError();
 }
-
-// Which form a chain takes.  Many chains (more than kWideCtas CTAs): one warp to 16
-// columns, one stage, two or three CTAs per SM.  Few: one warp with two stages for
-// heads of up to 64 in 16 bits (4.4 us a chunk against 5.1 with four warps), four warps for
-// wider heads and float32 (both chains of 4096 tokens, 128 x 128: 533 us against 621; seven
-// float32 sequences of 32 x 64: 67 against 100).
-template <typename Tin, int DKP>
-constexpr bool chain_split() { return sizeof(Tin) == 4 || DKP == 128; }
 
 // the segments' ends and the states that they start from (REV: and end with in reverse)
 template <typename Tin, int DKP, int NP, bool REV>
@@ -154,9 +180,11 @@ cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
 {
     if (delta_wide(p, false))
         return launch_wide_out<Tin, DKP, NP, NPP, 1>(p, st);
-    if constexpr (chain_split<Tin, DKP>())
-        return launch_split_out<Tin, DKP, NP, NPP>(p, st);
-    else
+    if constexpr (chain_split_out<Tin, DKP>()) {
+        if (chain_split<Tin, DKP>() || delta_split_f16(p))
+            return launch_split_out<Tin, DKP, NP, NPP>(p, st);
+    }
+    if constexpr (!chain_split<Tin, DKP>())
         return launch_wide_out<Tin, DKP, NP, NPP, 2>(p, st);
 }
 // Both chains of a backward pass in one launch while they do not fill the SMs

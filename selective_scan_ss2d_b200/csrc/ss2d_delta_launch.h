@@ -34,9 +34,9 @@ inline long long delta_units(const DeltaParams &p)
         return p.nseq;
     return p.cu ? p.nslots / p.SC + p.nseq : (long long)p.nseq * ((p.NC + p.SC - 1) / p.SC);
 }
-inline bool delta_wide(const DeltaParams &p, bool bwd)
-{
-    return (long long)((p.DV + 63) / 64) * p.H * delta_units(p) * (bwd ? 2 : 1) > kWideCtas;
-}
+inline long long delta_ctas(const DeltaParams &p) { return (long long)((p.DV + 63) / 64) * p.H * delta_units(p); }
+inline bool delta_wide(const DeltaParams &p, bool bwd) { return delta_ctas(p) * (bwd ? 2 : 1) > kWideCtas; }
+// float16 outputs by four warps to 16 columns: wide heads, and so few that two CTAs of 32 columns have an SM each
+inline bool delta_split_f16(const DeltaParams &p) { return !p.SC && delta_ctas(p) * 2 <= 148; }
 
 }  // namespace ss2d
