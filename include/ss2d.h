@@ -410,12 +410,13 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * sequence of no tokens gets h_last = h0.
  * All pointers DEVICE pointers of the current device (SS2D_ERR_PTR otherwise),
  * 16-byte aligned.  Asynchronous on `stream`; scratch (per 64 tokens and head 21 to
- * 32 KB, for float16 and float32 also 512 or 768 DKP bytes per key head, DKP = 64 or
+ * 32 KB, for float32 (and few float16) sequences also 768 (512) DKP bytes per key head, DKP = 64 or
  * 128, DK rounded up; for few long sequences three states per head and segment) comes
  * from the stream-ordered pool.  L < 2^31 - 64.
  *
  * Precision: the state and all arithmetic are float32 (products on the tensor
- * cores of operands split into bfloat16 parts that hold them to float32 accuracy);
+ * cores of operands split into bfloat16 or scaled float16 parts that hold them to
+ * float32 accuracy, the latter relative to the largest value of a state's column);
  * o is rounded once, on store.  Where o is 16 bits and no h_last is asked for,
  * intermediate values keep 16 bits of mantissa.  A value that is not finite
  * may reach every output of its sequence from its group of 64 tokens on. */

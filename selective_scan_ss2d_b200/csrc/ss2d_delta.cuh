@@ -367,23 +367,30 @@ __device__ __forceinline__ void mma_cols(float (&c0)[4], float (&c1)[4], const u
 // ---- float16 inputs as they are -----------------------------------------------
 // K and Q of float16 calls are one exact float16 operand each, where bfloat16 parts would
 // be two; what multiplies them is split into two float16 parts (22 bits) after
-// scaling by the power of two that brings the warp's largest value into 2^13 .. 2^14: two
-// products instead of five, and half the shared memory.  A value smaller than the largest
-// by 2^16 and more keeps fewer bits, but none is off by more than 2^-38 of the largest.
+// scaling each row (a column of DV) by the power of two that brings its largest value into
+// 2^13 .. 2^14: two products instead of five, and half the shared memory.  A value
+// smaller than its row's largest by 2^16 and more keeps fewer bits, but none is off by
+// more than 2^-38 of the largest.
 struct HalfScale {
-    float up, down;
+    float up[2], down[2];   // of the lane's rows
 };
 template <int N>
 __device__ __forceinline__ HalfScale half_scale(const float (&v)[N][4])
 {
-    float m = 0.f;   // a NaN is passed over here and stays one in its part
+    HalfScale s;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int r = 0; r < 2; ++r) {
+        float m = 0.f;   // a NaN is passed over here and stays one in its part
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            m = fmaxf(m, fabsf(v[n][j]));
-    const uint32_t e = max(__reduce_max_sync(0xffffffffu, __float_as_uint(m)) >> 23, 14u);
-    return {__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
+        for (int n = 0; n < N; ++n)
+            m = fmaxf(m, fmaxf(fabsf(v[n][2 * r]), fabsf(v[n][2 * r + 1])));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t e = max(__float_as_uint(m) >> 23, 14u);
+        s.up[r] = __uint_as_float((267u - e) << 23);
+        s.down[r] = __uint_as_float((e - 13u) << 23);
+    }
+    return s;
 }
 __device__ __forceinline__ void half_split(float x, float y, uint32_t &hi, uint32_t &lo)
 {
@@ -393,12 +400,13 @@ __device__ __forceinline__ void half_split(float x, float y, uint32_t &hi, uint3
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
-__device__ __forceinline__ void half_frag(const float (&c0)[4], const float (&c1)[4], float up, uint32_t (&a)[2][4])
+__device__ __forceinline__ void half_frag(const float (&c0)[4], const float (&c1)[4], const float (&up)[2],
+                                          uint32_t (&a)[2][4])
 {
-    half_split(c0[0] * up, c0[1] * up, a[0][0], a[1][0]);
-    half_split(c0[2] * up, c0[3] * up, a[0][1], a[1][1]);
-    half_split(c1[0] * up, c1[1] * up, a[0][2], a[1][2]);
-    half_split(c1[2] * up, c1[3] * up, a[0][3], a[1][3]);
+    half_split(c0[0] * up[0], c0[1] * up[0], a[0][0], a[1][0]);
+    half_split(c0[2] * up[1], c0[3] * up[1], a[0][1], a[1][1]);
+    half_split(c1[0] * up[0], c1[1] * up[0], a[0][2], a[1][2]);
+    half_split(c1[2] * up[1], c1[3] * up[1], a[0][3], a[1][3]);
 }
 __device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -412,7 +420,7 @@ __device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4],
 // otherwise in the scaled sum itself
 template <bool FROM0>
 __device__ __forceinline__ void mma_half(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[2][4],
-                                         const uint32_t (&b)[4], float down)
+                                         const uint32_t (&b)[4], const float (&down)[2])
 {
     if constexpr (FROM0) {
         float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -423,8 +431,8 @@ __device__ __forceinline__ void mma_half(float (&c0)[4], float (&c1)[4], const u
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            c0[j] = fmaf(d0[j], down, c0[j]);
-            c1[j] = fmaf(d1[j], down, c1[j]);
+            c0[j] = fmaf(d0[j], down[j >> 1], c0[j]);
+            c1[j] = fmaf(d1[j], down[j >> 1], c1[j]);
         }
     } else {
 #pragma unroll

@@ -264,7 +264,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                     for (int j = 0; j < 4; ++j)
                         R[n][j] = O[n][j] = 0.f;
                 // (K S)^T
-                [[maybe_unused]] HalfScale hs{1.f, 1.f};
+                [[maybe_unused]] HalfScale hs{{1.f, 1.f}, {1.f, 1.f}};
                 if constexpr (HALF)
                     hs = half_scale(S);
 #pragma unroll
@@ -293,7 +293,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                     for (int n = 0; n < 8; ++n)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            R[n][j] *= hs.down;
+                            R[n][j] *= hs.down[j >> 1];
                 }
                 if constexpr (MODE != kChainRev) {
 #pragma unroll
@@ -356,12 +356,12 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
                                                                      b * 16, ks * 2);
                             }
                         }
-                        const float os = HALF ? p.scale * hs.down : p.scale;
+                        const float os[2] = {p.scale * (HALF ? hs.down[0] : 1.f), p.scale * (HALF ? hs.down[1] : 1.f)};
 #pragma unroll
                         for (int n = 0; n < 8; ++n)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                O[n][j] *= os * eg[n * 8 + t2 + (j & 1)];
+                                O[n][j] *= os[j >> 1] * eg[n * 8 + t2 + (j & 1)];
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
                             if (ks >= NB)

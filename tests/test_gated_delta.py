@@ -527,6 +527,23 @@ def test_repeatable_streams_and_graphs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_channels_of_very_different_size(dtype):
+    """every value channel is a recurrence of its own: scaled by a power of two, it keeps its bits"""
+    a = make(2, 150, 1, 2, 64, 48)
+    t, _ = dev(dict(a, v=a["v"] / 64), dtype)
+    up = 2.0 ** (torch.arange(48) % 17).cuda()   # values of about 2^-6 .. 2^10, the same bits as the stored ones
+    u = dict(t, v=(t["v"].float() * up).to(t["v"].dtype))
+    assert torch.equal(t["v"].float() * up, u["v"].float())
+    o, h = binding.gated_delta_rule_fwd(**t, final_state=True)
+    o1, h1 = binding.gated_delta_rule_fwd(**u, final_state=True)
+    assert torch.equal(h * up[:, None].T, h1)
+    # float16 outputs below 2^-14 are rounded to multiples of 2^-24 before they are scaled here
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0
+    assert bool(((o.float() * up - o1.float()).abs() <= tiny * up).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("raw", [False, True])
 def test_another_stream_than_the_current_one(raw):
     """everything that a call writes, rows of no sequence among it, is written on its stream"""
