@@ -15,6 +15,7 @@
 //     dS^T <- e^{c_last} dS^T + (scale e^c dO)^T Q + dR^T K
 // It needs nothing of the forward chain, so that a backward pass runs both in
 // one launch.
+// float16 K and Q are multiplied as they are, by scaled float16 parts.
 //
 // A long chain of few heads would leave most SMs idle (three heads of 65536 tokens:
 // 1024 chunks one after the other, 4.2 ms).  Its chunks are cut into segments of SC.
@@ -57,7 +58,7 @@ struct ChainLayout {
 // of the segment that no other follows
 template <typename Tin, int DKP, int NW, int MODE, int NP, int NPP, int STAGES, bool LOCAL>
 __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool ident, long long units,
-                                            bool every = false)
+                                            bool every = false, unsigned z0 = blockIdx.z, unsigned zn = gridDim.z)
 {
     using Lay = ChainLayout<Tin, DKP, NW, MODE, NP, NPP, STAGES>;
     constexpr bool HALF = Lay::HALF;
@@ -70,7 +71,7 @@ __device__ __forceinline__ void delta_chain(const DeltaParams &p, int tile, bool
     const int dvw = (tile * NW + warp) * 16;   // first of the warp's DV columns
     const bool won = dvw < (LOCAL && ident ? p.DK : p.DV);
     __shared__ int ranked;
-    for (long long z = blockIdx.z; z < units; z += gridDim.z) {
+    for (long long z = z0; z < units; z += zn) {
         // packed sequences are taken by length, the longest first: the last chains to start are short ones
         long long unit = z;
         if (p.cu && !p.SC && p.nseq <= NT) {
@@ -541,15 +542,20 @@ __global__ void
 {
     delta_chain<Tin, DKP, NW, kChainOut, NP, NPP, STAGES, false>(p, blockIdx.x, false, units);
 }
-// one chain of the backward pass
-template <typename Tin, int DKP, int NW, int STAGES, int MODE>
+// all reverse chains, then all forward ones (the second half of blockIdx.z)
+template <typename Tin, int DKP, int NW, int STAGES>
 __global__ void
-    __launch_bounds__(NW * 32, (chain_ctas<ChainLayout<Tin, DKP, NW, MODE, 3, 3, STAGES>, DKP, STAGES>()))
-        delta_one_kernel(const DeltaParams p, long long units)
+    __launch_bounds__(NW * 32, (chain_ctas<ChainLayout<Tin, DKP, NW, kChainRev, 3, 3, STAGES>, DKP, STAGES>()))
+        delta_each_kernel(const DeltaParams p, long long units)
 {
-    delta_chain<Tin, DKP, NW, MODE, 3, 3, STAGES, false>(p, blockIdx.x, false, units);
+    const unsigned zn = gridDim.z / 2;
+    if (blockIdx.z < zn)
+        delta_chain<Tin, DKP, NW, kChainRev, 3, 3, STAGES, false>(p, blockIdx.x, false, units, false, blockIdx.z, zn);
+    else
+        delta_chain<Tin, DKP, NW, kChainState, 3, 3, STAGES, false>(p, blockIdx.x, false, units, false,
+                                                                     blockIdx.z - zn, zn);
 }
-// the forward chain and the reverse one, the longer one first
+// the forward chain and the reverse one side by side, the longer one first
 template <typename Tin, int DKP, int NW, int STAGES>
 __global__ void __launch_bounds__(NW * 32,
                                   (chain_ctas<ChainLayout<Tin, DKP, NW, kChainRev, 3, 3, STAGES>, DKP, STAGES>()))

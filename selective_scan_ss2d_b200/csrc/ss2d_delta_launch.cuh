@@ -21,9 +21,9 @@ cudaError_t delta_smem(void (*kern)(A...), int bytes)
 // heads of up to 64 in 16 bits (4.4 us a chunk against 5.1 with four warps), four warps for
 // wider heads and float32 (both chains of 4096 tokens, 128 x 128: 533 us against 621; seven
 // float32 sequences of 32 x 64: 67 against 100).  float16, whose one-warp form has fewer products,
-// takes four warps only for the outputs of few wide heads (4096 tokens, 32 chains: 389 us a call against
-// 488; 500 tokens, 128 chains 151 against 131; a backward pass of 32 chains 1298 against 1118,
-// segments 291 against 237).
+// takes four warps, and k and q in parts, only for the outputs of few wide heads (a call on 4096 tokens, 32
+// chains: 388 us against 488; 500 tokens, 128 chains 151 against 107; a backward pass of 32 chains 1298 against
+// 1087, 16384 tokens of 4 heads in segments 291 against 217).
 template <typename Tin, int DKP>
 constexpr bool chain_split_out() { return sizeof(Tin) == 4 || DKP == 128; }
 template <typename Tin, int DKP>
@@ -71,15 +71,17 @@ cudaError_t launch_wide_out(const DeltaParams &p, cudaStream_t st)
     kern<<<chain_grid(p, (p.DV + 63) / 64), 128, smem, st>>>(p, delta_units(p));
     return cudaGetLastError();
 }
-template <typename Tin, int DKP, int MODE>
-cudaError_t launch_wide_one(const DeltaParams &p, cudaStream_t st)
+template <typename Tin, int DKP>
+cudaError_t launch_wide_each(const DeltaParams &p, cudaStream_t st)
 {
-    constexpr int smem = ChainLayout<Tin, DKP, 4, MODE, 3, 3, 1>::bytes;
-    auto kern = delta_one_kernel<Tin, DKP, 4, 1, MODE>;
+    constexpr int smem = ChainLayout<Tin, DKP, 4, kChainRev, 3, 3, 1>::bytes;   // the larger of the two
+    auto kern = delta_each_kernel<Tin, DKP, 4, 1>;
     const cudaError_t e = delta_smem(kern, smem);
     if (e != cudaSuccess)
         return e;
-    kern<<<chain_grid(p, (p.DV + 63) / 64), 128, smem, st>>>(p, delta_units(p));
+    dim3 grid = chain_grid(p, (p.DV + 63) / 64);
+    grid.z = 2 * (grid.z < 32767 ? grid.z : 32767);
+    kern<<<grid, 128, smem, st>>>(p, delta_units(p));
     return cudaGetLastError();
 }
 template <typename Tin, int DKP>
@@ -187,16 +189,15 @@ cudaError_t launch_chain_out(const DeltaParams &p, cudaStream_t st)
     if constexpr (!chain_split<Tin, DKP>())
         return launch_wide_out<Tin, DKP, NP, NPP, 2>(p, st);
 }
-// Both chains of a backward pass in one launch while they do not fill the SMs
-// twice; beyond that one after the other: CTAs of both on an SM wait for
-// instructions (6144 chunks of 64 x 64 heads: 3 of 10 cycles a warp waited).
+// Both chains of a backward pass side by side while they do not fill the SMs twice;
+// beyond that one after the other: CTAs of both on an SM wait for instructions
+// (6144 chunks of 64 x 64 heads: 3 of 10 cycles a warp waited, 366 us; in two launches, each with its own last
+// wave, 292; in one launch with the reverse chains first 280).
 template <typename Tin, int DKP>
 cudaError_t launch_chain_both(const DeltaParams &p, cudaStream_t st)
 {
-    if (delta_wide(p, true)) {
-        const cudaError_t e = launch_wide_one<Tin, DKP, kChainState>(p, st);
-        return e != cudaSuccess ? e : launch_wide_one<Tin, DKP, kChainRev>(p, st);
-    }
+    if (delta_wide(p, true))
+        return launch_wide_each<Tin, DKP>(p, st);
     if constexpr (chain_split<Tin, DKP>())
         return launch_split_both<Tin, DKP>(p, st);
     else
