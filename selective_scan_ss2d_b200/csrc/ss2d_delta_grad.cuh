@@ -27,7 +27,7 @@
 // chunks of 64 x 64 heads).  With two it took 412; of a CTA's 37,000 clocks the products
 // had 16,000, the sums of E 6,500, most of them in branches, and staging 4,500: a tile of
 // S^T or V' read once for two products, selects in place of the branches and dc
-// and dbeta by two warps made it 364 (31,000 clocks; the tensor pipe at 38 %).
+// and dbeta by two warps made it 364 (31,000 clocks; the tensor pipe at 37 %, issue at 43 %).
 #pragma once
 
 #include "ss2d_delta_chain.cuh"
