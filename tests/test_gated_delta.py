@@ -544,6 +544,25 @@ def test_channels_of_very_different_size(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_no_tokens_and_no_sequences(dtype):
+    """states pass through sequences of nothing; tokens without sequences have no gradient"""
+    def call(L):
+        new = lambda *s: torch.ones(*s, dtype=DT[dtype], device="cuda")  # noqa: E731
+        g = torch.ones(1, L, 2, device="cuda")
+        return dict(q=new(1, L, 2, 16), k=new(1, L, 2, 16), v=new(1, L, 2, 32), g=g, beta=g)
+
+    h0 = torch.rand(3, 2, 16, 32, device="cuda")
+    t, cu = call(0), torch.zeros(4, dtype=torch.int32, device="cuda")
+    o, h = binding.gated_delta_rule_fwd(**t, h0=h0, cu_seqlens=cu, final_state=True)
+    gr = binding.gated_delta_rule_bwd(**t, do=t["v"], h0=h0, dh_last=2 * h0, cu_seqlens=cu)
+    assert o.shape == t["v"].shape and torch.equal(h, h0) and torch.equal(gr["dh0"], 2 * h0)
+    t = call(70)
+    gr = binding.gated_delta_rule_bwd(**t, do=t["v"], cu_seqlens=cu[:1])
+    assert not any(gr[n].any() for n in ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("raw", [False, True])
 def test_another_stream_than_the_current_one(raw):
     """everything that a call writes, rows of no sequence among it, is written on its stream"""
