@@ -650,6 +650,9 @@ __global__ void __launch_bounds__(M == kNormAny ? 512 : 256, M == kNormAny ? 1 :
         norm_stats2<E>([&](float (&v)[E]) { rr.get(v); }, pre ? p.pre : kNormNone,
                        [&](float (&v)[E]) { xr.get(v); }, post ? p.post : kNormNone, D, p.eps,
                        sum, in, mean, rs);
+        // a team past the last row holds zeros: with eps = 0 its 1 / sqrt is infinite, and 0 * inf would go into the
+        // column sums
+        rs = live ? rs : make_float2(0.f, 0.f);
         // G: the gradient of r'
         if (pre) {
             rr.get(a);
