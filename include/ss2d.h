@@ -498,8 +498,10 @@ int block_norm_fwd(const void *x, const void *z, const void *r, const float *s,
  * differentiated at that value).  Writes dx, dz (dtype, contiguous; dz when z
  * is given), dr (r_dtype; NULL = not wanted) and, where not NULL and where the
  * call has the part, the float32 sums over the rows ds, dw_post, db_post,
- * dw_pre, db_pre (D): each in a fixed order, the same bits on every call.
- * With no rows the sums are zero.  dr may be dr_out, and dx may be x if x is
+ * dw_pre, db_pre (D): each in a fixed order, the same bits on every call. ds
+ * belongs to s, the others to their norm (with or without a weight): what belongs
+ * to a part that the call does not have is left as it was.  With no rows the
+ * sums are zero.  dr may be dr_out, and dx may be x if x is
  * contiguous; otherwise no output may overlap an input or another output.
  * Scratch for the partial sums (8880 * D bytes at most, none for a few rows)
  * comes from the stream-ordered pool. */

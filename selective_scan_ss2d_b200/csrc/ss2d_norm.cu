@@ -208,8 +208,8 @@ int block_norm_bwd(const void *x, const void *z, const void *r_out, const float 
     if (rc != SS2D_OK || D == 0)
         return rc;
     // column sums of a part that the call does not have are not written
-    const ss2d::NormSums out{{ds, post ? dw_post : nullptr, pre ? dw_pre : nullptr, post ? db_post : nullptr,
-                              pre ? db_pre : nullptr}};
+    const ss2d::NormSums out{{s ? ds : nullptr, post ? dw_post : nullptr, pre ? dw_pre : nullptr,
+                              post ? db_post : nullptr, pre ? db_pre : nullptr}};
     for (int i = 0; i < ss2d::kNormCols; ++i)
         p.cols |= (out.out[i] ? 1 : 0) << i;
     const void *sums[] = {out.out[0], out.out[1], out.out[2], out.out[3], out.out[4]};

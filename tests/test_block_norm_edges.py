@@ -1,5 +1,5 @@
 """The block norms at the edges of what their calls allow: eps = 0 where rows
-do not fill the last step's teams."""
+do not fill the last step's teams, and sums of parts that a call does not have."""
 from __future__ import annotations
 
 import functools
@@ -49,3 +49,22 @@ def test_gradient_of_a_length_normalisation(how):
     # (360 + 160) additions and 64 operations on each term, see test_block_norm
     err = np.abs(g["dw_post"].double().cpu().numpy() - ref["dw_post"])
     assert np.all(err <= (360 + 160 + 64) * tb.U * ref["abs"]["dw_post"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [0, 5, 5003])   # no kernel, one cluster, partial sums
+@pytest.mark.parametrize("post", ["none", "rms"])
+def test_sums_of_parts_that_a_call_does_not_have_are_left(rows, post):
+    """the C call with every output given, and no s and no second norm: ds, dw_pre and db_pre keep what they held"""
+    D, lib = 64, binding.lib()
+    x, d, dx = (torch.ones(max(rows, 1), D, device="cuda") for _ in range(3))
+    w = torch.ones(D, device="cuda")
+    sums = {n: torch.full((D,), 7.0, device="cuda") for n in ("ds", "dw_post", "db_post", "dw_pre", "db_pre")}
+    p = lambda t: t.data_ptr()  # noqa: E731
+    rc = lib.block_norm_bwd(p(x), None, None, None, p(w), None, None, p(d), None, p(dx), None, None,
+                            *map(p, sums.values()), rows, D, 1, D, D, binding.NORMS[post], 0, 1e-5, 0, 0, None)
+    torch.cuda.synchronize()
+    assert rc == 0
+    has = ("dw_post", "db_post") if post != "none" else ()
+    for n, v in sums.items():
+        assert bool((v != 7).all()) if n in has else bool((v == 7).all()), n
