@@ -534,7 +534,9 @@ def _on(device, stream):
     """Makes a call's new tensors, and fills them, on the stream that the call runs on."""
     if stream is None:
         return _HERE
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):   # the default stream's handle is 0, of which ExternalStream would make another stream
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _token_stride(t, name):

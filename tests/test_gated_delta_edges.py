@@ -1,0 +1,27 @@
+"""The gated delta rule at the edges of what its calls allow: the default
+stream by its handle."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import test_gated_delta as td
+from selective_scan_ss2d_b200 import binding
+
+
+@pytest.mark.gpu
+def test_default_stream_by_its_handle():
+    """stream = 0 is the default stream, for a call's kernels and for the zeros of rows in no sequence"""
+    t, _ = td.dev(td.make(1, 150, 1, 2, 32, 32), "bf16")
+    do = torch.ones_like(t["v"])
+    cu = torch.tensor([7, 60, 120], dtype=torch.int32).cuda()
+    assert torch.cuda.default_stream().cuda_stream == 0
+    want = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu)
+    busy = [torch.cuda.Stream() for _ in range(64)]   # whatever other stream a call would use is behind
+    torch.cuda.synchronize()
+    for s in busy:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+    got = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu, stream=0)
+    torch.cuda.synchronize()
+    assert all(got[n] is None or torch.equal(got[n], want[n]) for n in want)
