@@ -609,7 +609,8 @@ def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=No
     q, k (B, L, HK, DK), v (B, L, H, DV) of one dtype, heads packed and tokens at
     any stride; g, beta (B, L, H) float32; h0 (sequences, H, DK, DV) float32.
     cu_seqlens (int32, device): B = 1 and the tokens of several sequences packed;
-    tokens in none of them leave o as it was.  scale defaults to DK ** -0.5; reverse
+    rows of tokens in none of them are left as they were in an o that is given and
+    zero in a new one.  scale defaults to DK ** -0.5; reverse
     reads every sequence from its end.  Returns (o, h_last): o (B, L, H, DV) of
     q's dtype, h_last like h0, None unless final_state or h_last is given (it may
     be h0).  Device tensors only."""
@@ -628,6 +629,8 @@ def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=No
     with _on(q.device, stream):
         if o is None:
             o = _new(v, v.dtype)
+            if cu_seqlens is not None:   # as in the backward pass
+                o.zero_()
         if h_last is None and final_state:
             h_last = torch.empty(sdims, dtype=torch.float32, device=q.device)
     rc = lib().gated_delta_rule_fwd(_raw(q), _raw(k), _raw(v), _raw(g), _raw(beta), _raw(h0), _raw(o),

@@ -1,5 +1,5 @@
 """The gated delta rule at the edges of what its calls allow: the default
-stream by its handle."""
+stream by its handle, rows of no sequence in a new output."""
 from __future__ import annotations
 
 import pytest
@@ -25,3 +25,15 @@ def test_default_stream_by_its_handle():
     got = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu, stream=0)
     torch.cuda.synchronize()
     assert all(got[n] is None or torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,cu", [(150, [7, 60, 120]), (150, [0, 149]), (150, [3]), (4, [1, 2]), (70, [70, 70])])
+def test_rows_of_no_sequence_are_zero_in_a_new_output(L, cu):
+    t, _ = td.dev(td.make(1, L, 1, 2, 32, 32), "bf16")
+    for _ in range(4):   # what the allocator hands out next holds NaN
+        torch.full_like(t["v"], float("nan"))
+    o, _ = binding.gated_delta_rule_fwd(**t, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert not o[0, :cu[0]].any() and not o[0, cu[-1]:].any()
+    assert bool(o[0, cu[0]:cu[-1]].any()) == (cu[-1] > cu[0])
