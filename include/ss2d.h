@@ -431,7 +431,8 @@ int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const floa
  * float32 or NULL (0).  Writes dq, dk (tokens, HK, DK) and dv (tokens, H, DV) in dtype,
  * contiguous, the gradients of shared key heads summed over their value heads in
  * a fixed order; dg, dbeta (tokens, H) float32; dh0 (nseq, H, DK, DV) float32 or NULL
- * (not wanted; may be dh_last).  The forward's other arguments and rules hold.
+ * (not wanted; may be dh_last).  The forward's other arguments and rules hold; key heads
+ * without value heads (HK > 0, H = 0) have no gradient here (SS2D_ERR_HEADS).
  * The states are computed again from the inputs and kept in scratch: per 64 tokens
  * and head 8 * DKP * DV + 512 * DV + 32000 bytes besides the forward's, from the
  * stream-ordered pool.  No atomics: the same bits on every call. */

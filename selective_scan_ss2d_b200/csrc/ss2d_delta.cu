@@ -253,6 +253,8 @@ int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const floa
     c.dtype = dtype;
     c.st = static_cast<cudaStream_t>(stream);
     int rc = validate(c);
+    if (rc == SS2D_OK && H == 0 && HK > 0)   // no kernel runs that could write dq and dk
+        rc = SS2D_ERR_HEADS;
     if (rc != SS2D_OK || nseq == 0 || H == 0 || (p.T == 0 && !dh0))
         return rc;
     const void *opt[] = {h0, dh_last, dh0, cu_seqlens};

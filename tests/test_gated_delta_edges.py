@@ -1,5 +1,5 @@
 """The gated delta rule at the edges of what its calls allow: the default
-stream by its handle, rows of no sequence in a new output."""
+stream by its handle, rows of no sequence in a new output, no value heads."""
 from __future__ import annotations
 
 import pytest
@@ -7,6 +7,16 @@ import torch
 
 import test_gated_delta as td
 from selective_scan_ss2d_b200 import binding
+
+lib = td.lib   # the fixture: the built library
+
+
+def test_backward_without_value_heads_is_refused(lib):
+    """nothing would write dq and dk"""
+    keep, p = td.ptr()
+    assert td._bwd(lib, p, HK=1, H=0, vs=0) == -14
+    assert td._bwd(lib, p, HK=0, H=0, qs=0, ks=0, vs=0) == 0
+    assert td._fwd(lib, p, HK=1, H=0, vs=0) == 0   # an output of no heads
 
 
 @pytest.mark.gpu
