@@ -1,12 +1,26 @@
 """The gated delta rule at the edges of what its calls allow: the default
-stream by its handle, rows of no sequence in a new output, no value heads."""
+stream by its handle, rows of no sequence in a new output, no value heads; and
+how far off it is as a whole, in every form of the chain and for many of them.
+
+What is kept in float32 is off by less than WHOLE of its L2 norm.  A product of
+three-part operands truncates once at its full size (2^-23, the small parts are summed
+first) and is joined by rounding additions, up to eight to a sum, whose errors of
+2^-24 add like sqrt(8); a result is at most six such sums in a row, none of which
+lets an error grow (|k| <= 1, beta <= 1, g <= 0): 6 * (2^-23 + sqrt(8) * 2^-24) = 1.7e-6 <
+2^-19.  Two scaled float16 parts hold 2^-23 of a column's largest value, four times
+its root mean square: 2^-21 / sqrt(3) for each of the six, below 2^-19 as well.  Two bf16
+parts, or parts summed where the whole sum truncates each of them, do not reach it."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 import test_gated_delta as td
+from oracle import gated_delta_np as onp
 from selective_scan_ss2d_b200 import binding
+
+WHOLE = 2.0 ** -19
 
 lib = td.lib   # the fixture: the built library
 
@@ -47,3 +61,110 @@ def test_rows_of_no_sequence_are_zero_in_a_new_output(L, cu):
     torch.cuda.synchronize()
     assert not o[0, :cu[0]].any() and not o[0, cu[-1]:].any()
     assert bool(o[0, cu[0]:cu[-1]].any()) == (cu[-1] > cu[0])
+
+
+def whole(got, ref, what, of=None):
+    """off by WHOLE of the reference's L2 norm (or of `of`'s, whose sum the reference is)"""
+    n = float(np.linalg.norm(ref if of is None else np.maximum(np.abs(ref), of)))
+    err = float(np.linalg.norm(got.double().cpu().numpy().reshape(ref.shape) - ref))
+    assert err <= WHOLE * n, f"{what}: {err / n:.2e}"
+
+
+def run(a, dtype, cu=None, reverse=False):
+    """forward, backward, and forward without states, against the oracle sequence by sequence"""
+    t, f = td.dev(a, dtype)
+    B, L, HK, DK = a["q"].shape
+    H, DV = a["v"].shape[2:]
+    bounds = [L * b for b in range(B + 1)] if cu is None else list(cu)
+    nseq = len(bounds) - 1
+    rng = np.random.default_rng([nseq, L, H])
+    new = lambda dt, *s: torch.from_numpy(rng.standard_normal(s)).to(dt).cuda()  # noqa: E731
+    h0, dh = 0.5 * new(torch.float32, nseq, H, DK, DV), 0.5 * new(torch.float32, nseq, H, DK, DV)
+    do = new(td.DT[dtype], B, L, H, DV)
+    kw = dict(cu_seqlens=None if cu is None else torch.tensor(bounds, dtype=torch.int32).cuda(), reverse=reverse)
+    o, h = binding.gated_delta_rule_fwd(**t, h0=h0, final_state=True, **kw)
+    g = binding.gated_delta_rule_bwd(**t, do=do, h0=h0, dh_last=dh, **kw)
+    o2, none = binding.gated_delta_rule_fwd(**t, h0=h0, **kw)
+    torch.cuda.synchronize()
+    n64 = lambda x: x.double().cpu().numpy()  # noqa: E731
+    fh, fdh, fdo = n64(h0), n64(dh), n64(do).reshape(f["v"].shape)
+    ref = {n: np.zeros_like(f[m]) for n, m in (("o", "v"), ("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"),
+                                               ("dbeta", "g"))}
+    ref["h"], ref["dh0"] = np.zeros_like(fh), np.zeros_like(fh)
+    amp = np.zeros(f["g"].shape)   # what dg is a sum of: |q||dq| + |k||dk| from a token to its chunk's end
+    for n in range(nseq):
+        at = slice(bounds[n], bounds[n + 1])
+        x, one = {m: v[at] for m, v in f.items()}, [0, bounds[n + 1] - bounds[n]]
+        ref["o"][at], rh, _ = onp.forward(**x, cu=one, h0=fh[n:n + 1], reverse=reverse)
+        ref["h"][n] = rh[0]
+        r = onp.backward(**x, cu=one, do=fdo[at], h0=fh[n:n + 1], dh_last=fdh[n:n + 1], reverse=reverse)
+        for m in ("dq", "dk", "dv", "dg", "dbeta"):
+            ref[m][at] = r[m]
+        ref["dh0"][n] = r["dh0"][0]
+        dot = sum(np.abs(x[m] * r["d" + m]).sum(-1).repeat(H // HK, 1) for m in "qk")
+        dot = dot[::-1] if reverse else dot   # in the order of reading
+        sums = np.concatenate([dot[i:i + 64][::-1].cumsum(0)[::-1] for i in range(0, len(dot), 64)] or [dot])
+        amp[at] = sums[::-1] if reverse else sums
+    names = [("h", h, None), ("dg", g["dg"], amp), ("dbeta", g["dbeta"], None), ("dh0", g["dh0"], None)]
+    if dtype == "f32":
+        names += [("o", o, None)] + [(m, g[m], None) for m in ("dq", "dk", "dv")]
+    for m, got, of in names:
+        whole(got, ref[m], m, of)
+    # 16-bit outputs: their rounding, and by element
+    M = td.mag(ref["o"], f["v"])
+    td.near(o, ref["o"], td.DT[dtype], td.FINE, M, "o")
+    assert none is None
+    td.near(o2, ref["o"], td.DT[dtype], td.FINE if dtype == "f32" else td.COARSE, M, "o without states")
+    for m in ("dq", "dk", "dv"):
+        td.near(g[m], ref[m], td.DT[dtype], td.FINE if dtype == "f32" else td.COARSE / 2, td.mag(ref[m]), m)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("HK,H,DK,DV,L", [(1, 2, 64, 64, 200), (1, 2, 128, 128, 200), (2, 2, 48, 80, 130),
+                                          (1, 1, 64, 48, 2100), (1, 1, 128, 64, 2090)])
+def test_float32_results_as_a_whole(HK, H, DK, DV, L, dtype):
+    """few chains, the last two cut into segments"""
+    run(td.make(1 if L > 1000 else 2, L, HK, H, DK, DV, decay=0.3), dtype, reverse=L == 130)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("HK,DK", [(3, 64), (1, 128)])
+def test_many_chains(HK, DK, dtype):
+    """300 CTAs of 64 columns to a direction: more than two for each SM"""
+    run(td.make(50, 70, HK, 3, DK, 80), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nseq,DK,DV", [(120, 32, 16), (200, 64, 32), (290, 96, 16), (600, 32, 48)])
+@pytest.mark.parametrize("dtype,reverse", [("bf16", True), ("f16", False), ("f32", False)])
+def test_many_packed_sequences(nseq, DK, DV, dtype, reverse):
+    """as many as a CTA has threads and more, ragged, some of no tokens"""
+    rng = np.random.default_rng(nseq)
+    lens = rng.integers(0, 24, nseq) * (rng.random(nseq) < 0.9)
+    lens[:3] = 0, 90, 64
+    cu = np.concatenate([[0], lens.cumsum()])
+    run(td.make(1, int(cu[-1]), 1, 1, DK, DV), dtype, cu=cu, reverse=reverse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cu", [None, [0, 0, 40, 41, 230], [0, 2100, 2100, 2300]])
+def test_scratch_of_an_earlier_call_is_not_read(cu, dtype):
+    """calls on NaN before it leave NaN in the scratch that a call gets next; its bits stay the same"""
+    L = cu[-1] if cu else 101
+    t, _ = td.dev(td.make(1 if cu else 3, L, 1, 2, 64, 80), dtype)
+    bad = {n: torch.full_like(v, float("nan")) for n, v in t.items()}
+    kw = dict(cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int32).cuda())
+    do = torch.ones_like(t["v"])
+
+    def call(x, d):
+        o, h = binding.gated_delta_rule_fwd(**x, final_state=True, **kw)
+        return [o, h, binding.gated_delta_rule_fwd(**x, **kw)[0], *binding.gated_delta_rule_bwd(**x, do=d, **kw).values()]
+
+    want = call(t, do)
+    for _ in range(2):
+        assert all(v is None or torch.isnan(v).any() for v in call(bad, bad["v"]))
+        got = call(t, do)
+        assert all(w is None or (torch.isfinite(w).all() and torch.equal(w, v)) for w, v in zip(want, got))
