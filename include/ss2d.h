@@ -384,8 +384,12 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  *   S_t = exp(g_t) S_{t-1} + k_t d_t^T            S (DK, DV)
  *   o_t = scale * S_t^T q_t
  * so that without decay (g = 0), with |k| = 1 and beta = 1, S_t^T k_t = v_t.
- * Keys are normally scaled to |k| <= 1 by the caller and g <= 0, 0 <= beta <= 1;
- * the recurrence is computed as written for any values (it grows where it grows).
+ * Keys are normally scaled to |k| <= 1 by the caller and g <= 0, 0 <= beta <= 1.
+ * Other keys and betas are computed as written (the states grow where the recurrence
+ * grows), and so is g > 0 in the one-token form and in forward calls of up to 4 tokens. Longer
+ * calls work by groups of 64 tokens, with exp of sums of g in a group: what such a sum lets
+ * grow, it lets errors grow by too, also where the next keys replace the value, and above
+ * 88 it overflows; so they are meant for g <= 0, or sums of a few units.
  * g = -infinity forgets the state; below -200 exp(g) is 0 in float32 and g is read
  * as -200.
  *

@@ -613,7 +613,8 @@ def gated_delta_rule_fwd(q, k, v, g, beta, h0=None, *, scale=None, cu_seqlens=No
     zero in a new one.  scale defaults to DK ** -0.5; reverse
     reads every sequence from its end.  Returns (o, h_last): o (B, L, H, DV) of
     q's dtype, h_last like h0, None unless final_state or h_last is given (it may
-    be h0).  Device tensors only."""
+    be h0).  g <= 0, or sums over 64 tokens of a few units: errors grow with exp of
+    them.  Device tensors only."""
     dims, strides, dt = _delta_prepare(q, k, v, g, beta, "gated_delta_rule_fwd")
     if q.dim() != 4:
         raise ValueError("q must be (B, L, HK, DK)")

@@ -168,3 +168,35 @@ def test_scratch_of_an_earlier_call_is_not_read(cu, dtype):
         assert all(v is None or torch.isnan(v).any() for v in call(bad, bad["v"]))
         got = call(t, do)
         assert all(w is None or (torch.isfinite(w).all() and torch.equal(w, v)) for w, v in zip(want, got))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_that_grow(dtype):
+    """g above 0: errors are FINE of the largest value, times what a group of 64 tokens lets grow"""
+    a = td.make(2, 150, 1, 2, 64, 32)
+    a["g"] = np.random.default_rng(3).uniform(-0.1, 0.2, a["g"].shape)
+    t, f = td.dev(a, dtype)
+    o, h = binding.gated_delta_rule_fwd(**t, final_state=True)
+    torch.cuda.synchronize()
+    ro, rh, _ = onp.forward(**f, cu=[0, 150, 300])
+    c = np.concatenate([np.zeros((1, 2)), f["g"].cumsum(0)])
+    grow = max(float((c[i + 1:i + 65] - c[i]).max()) for i in range(300))
+    td.near(o, ro, td.DT[dtype], td.FINE * np.exp(grow), td.mag(ro, f["v"]), "o")
+    td.near(h, rh, torch.float32, td.FINE * np.exp(grow), td.mag(rh, f["v"]), "h_last")
+
+
+@pytest.mark.gpu
+def test_replaced_values_under_growth():
+    """one key, beta = 1: S^T k = v whatever g; by groups errors grow with exp(64 g), token by token they do not"""
+    k = torch.zeros(1, 64, 1, 32, device="cuda")
+    k[..., 0] = 1
+    v, one = torch.ones(1, 64, 1, 16, device="cuda"), torch.ones(1, 64, 1, device="cuda")
+    o, _ = binding.gated_delta_rule_fwd(k, k, v, 0.05 * one, one, scale=1.0, final_state=True)
+    torch.cuda.synchronize()
+    assert float((o - 1).abs().max()) <= td.FINE * np.exp(64 * 0.05)
+    state = torch.zeros(1, 1, 32, 16, device="cuda")
+    for t in range(64):
+        got = binding.gated_delta_rule_step(k[:, t], k[:, t], v[:, t], 2 * one[:, 0], one[:, 0], state, scale=1.0)
+        # a value of 1 grows to e^2 and is taken off again: three roundings of e^2 at most
+        assert float((got - 1).abs().max()) <= 3 * np.exp(2.0) * 2.0 ** -23
