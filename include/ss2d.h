@@ -413,10 +413,13 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * NULL = not wanted; h_last may be h0, otherwise no output may overlap an input.  A
  * sequence of no tokens gets h_last = h0.
  * All pointers DEVICE pointers of the current device (SS2D_ERR_PTR otherwise),
- * 16-byte aligned.  Asynchronous on `stream`; scratch (per 64 tokens and head 21 to
- * 32 KB, for float32 (and few float16) sequences also 768 (512) DKP bytes per key head, DKP = 64 or
- * 128, DK rounded up; for few long sequences three states per head and segment) comes
- * from the stream-ordered pool.  L < 2^31 - 64.
+ * 16-byte aligned.  Asynchronous on `stream`.  Scratch comes from the stream-ordered
+ * pool, with DKP = 64 or 128, DK rounded up: per group of 64 tokens (ceil(L / 64) to a
+ * sequence; packed, L / 64 in all and one more for every sequence, also one of no tokens) and
+ * head 21 to 32 KB; for float32 inputs also 768 DKP bytes per group and key head, for few
+ * wide float16 heads 512 DKP; and for few long sequences, whose chains are cut into
+ * some 148 / (H ceil(DV / 64)) segments in all and one or two more to a sequence, 8 DKP DV +
+ * 6 DKP^2 bytes per segment and head.  None for up to 4 tokens.  L < 2^31 - 64.
  *
  * Precision: the state and all arithmetic are float32 (products on the tensor
  * cores of operands split into bfloat16 or scaled float16 parts that hold them to
@@ -437,8 +440,9 @@ int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const floa
  * a fixed order; dg, dbeta (tokens, H) float32; dh0 (nseq, H, DK, DV) float32 or NULL
  * (not wanted; may be dh_last).  The forward's other arguments and rules hold; key heads
  * without value heads (HK > 0, H = 0) have no gradient here (SS2D_ERR_HEADS).
- * The states are computed again from the inputs and kept in scratch: per 64 tokens
- * and head 8 * DKP * DV + 512 * DV + 32000 bytes besides the forward's, from the
+ * The states are computed again from the inputs and kept in scratch: per group of 64
+ * tokens and head 8 DKP DV + 512 DV + 32000 bytes in all, for float32 inputs 768 DKP bytes per
+ * group and key head besides, and 16 DKP DV + 6 DKP^2 bytes per segment and head, from the
  * stream-ordered pool.  No atomics: the same bits on every call. */
 int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const float *g,
                          const float *beta, const float *h0, const void *dout,
