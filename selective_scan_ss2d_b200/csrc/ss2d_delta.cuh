@@ -14,16 +14,21 @@
 // T and P of every chunk are independent of the states and come from
 // delta_prep_kernel; the states are a chain over the chunks (ss2d_delta_chain.cuh).
 //
-// Precision.  The products run on the tensor cores with bfloat16 operands and
-// float32 sums, but nothing is rounded to bfloat16: a float32 operand is the
-// exact sum of three bfloat16 parts (8 bits each), a float16 value of two,
-// and a product of two split operands is the sum of the partial products
+// Precision.  The products run on the tensor cores with 16-bit operands and float32
+// sums.  A float32 operand is split into bfloat16 parts of 8 bits each: three hold
+// it exactly, and a product of two split operands is the sum of the partial products
 // whose parts' indices add up to less than the number of parts kept (3: what
-// is left out is below 2^-24 of the product, as a float32 rounding is; 2:
-// below 2^-16, used where the result is only rounded to 16 bits).  bfloat16
-// inputs are one part: q.k needs one product and k.S three.  States, sums of
-// g (in double within a chunk: differences of near tokens behind a large
-// sum keep float32 accuracy) and everything elementwise stay float32.
+// is left out is below 2^-24 of the product, as a float32 rounding is).  Two parts
+// hold 16 bits and leave out 2^-16 of a product.  They are used where
+// only results that are rounded to 16 bits are made of them: P in every
+// forward pass of 16-bit inputs, S, X, V' and T there if no last state is asked for, and
+// the products with GP and GA in the gradients dq and dk of 16-bit inputs.  bfloat16
+// inputs are one part: q.k needs one product and k.S three.  float16 k and q are
+// operands as they are against two scaled float16 parts, 22 bits of a row's largest value,
+// in the chains (see below); in the outputs of few wide heads and in the gradient kernel they are
+// two bfloat16 parts, which hold them exactly.  States, sums of g (in double within a
+// chunk: differences of near tokens behind a large sum keep float32
+// accuracy) and everything elementwise stay float32, the exponentials on ex2.approx (2^-22).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -505,7 +510,7 @@ constexpr int kRecurThreads = 256;
 
 // ROWS: rows of the state per thread
 template <typename Tin, int ROWS>
-__global__ void __launch_bounds__(kRecurThreads, ROWS <= 8 ? 4 : 2) delta_recur_kernel(const DeltaParams p, int DVT)
+__global__ void __launch_bounds__(kRecurThreads, 4) delta_recur_kernel(const DeltaParams p, int DVT)
 {
     __shared__ float sk[kDeltaMaxDK], sq[kDeltaMaxDK];
     __shared__ __align__(16) float red[2][kRecurThreads][4];

@@ -7,7 +7,8 @@
 //     one token block (16 tokens) of R, X, V' and the output (dV', dX in reverse), and
 //     a quarter of DK of the group's state, in float32 accumulators,
 // and what the others need of it as an A operand (the parts of S, X, V', e^{..} V') goes
-// through shared memory, split once by its owner.  A group meets four times a chunk.
+// through shared memory, split once by its owner.  A chunk has three meetings of a group (four in
+// reverse) and two of the CTA.
 // Every scheduler has four warps to choose from, whose blocks are rotated from group to
 // group, since T and P give a block between one and four products.
 // K of the next chunk is copied during this one; Q, T, P and V of this chunk

@@ -20,12 +20,15 @@
 // and its statistics are exact two-pass sums: the mean first, then the sum of
 // squares about it.  Rows of 64 16-bit values are 8 lanes of one 16-byte
 // vector each, four rows to a warp; teams of more than a warp sum through
-// shared memory.  Every kernel is bound by the bytes of its rows.
+// shared memory.  What bounds a form is said at its kernel: the bytes of its rows
+// in the gated head norm, which runs at four fifths of the copy rate, before
+// them two waves of CTAs in wider forward rows, and the rounds of sums in the backward.
 //
 // The backward's column sums (weights, biases, scale) are kept in registers
-// over all the rows that a team visits, summed over the CTA's teams in
-// order, written as one partial per CTA and summed by a second kernel in
-// order: the same bits on every call.
+// over all the rows that a team visits and summed over the CTA's teams in
+// order.  The CTAs' sums are partials that a second kernel adds up in order or,
+// for few rows, stay in the shared memory of one cluster, which adds them up
+// itself: the same bits on every call either way.
 #pragma once
 
 #include <cuda_bf16.h>
