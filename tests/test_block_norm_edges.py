@@ -68,3 +68,39 @@ def test_sums_of_parts_that_a_call_does_not_have_are_left(rows, post):
     has = ("dw_post", "db_post") if post != "none" else ()
     for n, v in sums.items():
         assert bool((v != 7).all()) if n in has else bool((v == 7).all()), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,D,dtype", [(9, 64, "bf16"), (700, 191, "f32"), (5003, 192, "bf16"), (301, 4100, "f16")])
+def test_gradients_in_place(rows, D, dtype):
+    """dx in x's place and dr in dr_out's, as the header allows: the bits of separate ones"""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    dt, lib = tb.DT[dtype], binding.lib()
+    x, z, r, d, dy = (torch.randn(rows, D, device="cuda", generator=gen).to(dt) for _ in range(5))
+    w = torch.rand(D, device="cuda", generator=gen)
+    want = binding.block_norm_bwd(x, d, dy, r_out=r, z=z, s=w, post="rms", w_post=w, pre="layer", w_pre=w, b_pre=w)
+    dz, sums = torch.empty_like(z), [torch.empty_like(w) for _ in range(4)]
+    p = lambda t: t.data_ptr()  # noqa: E731
+    ds, dwq, dwp, dbp = sums
+    rc = lib.block_norm_bwd(p(x), p(z), p(r), p(w), p(w), None, p(w), p(d), p(dy), p(x), p(dz), p(d), p(ds), p(dwq),
+                            None, p(dwp), p(dbp), rows, D, 1, D, D, 1, 2, 1e-5, binding._DTYPES[dt], binding._DTYPES[dt],
+                            None)
+    torch.cuda.synchronize()
+    assert rc == 0
+    for n, v in (("dx", x), ("dr", d), ("dz", dz), ("ds", ds), ("dw_post", dwq), ("dw_pre", dwp)):
+        assert torch.equal(want[n], v), n
+
+
+@pytest.mark.gpu
+def test_more_rows_than_32_bits_count():
+    """2^31 + 8 rows of one value, in groups of two and packed: the last ones, and a column sum of all"""
+    M = (1 << 30) + 4
+    wide = torch.zeros(M, 4, dtype=torch.bfloat16, device="cuda")
+    x = wide[:, :2].unflatten(1, (2, 1))
+    x[-3:] = torch.tensor([[1.0, -2.0], [3.0, 4.0], [5.0, -6.0]], device="cuda").bfloat16()[..., None]
+    s = torch.full((1,), 2.0, device="cuda")
+    r, _ = binding.block_norm_fwd(x, s=s)
+    assert torch.equal(r[-3:], 2 * x[-3:]) and not r[:1000].any() and not r[-1000:-3].any()
+    g = binding.block_norm_bwd(x, r, s=s, residual=False)
+    torch.cuda.synchronize()
+    assert torch.equal(g["dx"][-3:], 2 * r[-3:]) and float(g["ds"]) == 2 * (1 + 4 + 9 + 16 + 25 + 36)

@@ -12,6 +12,8 @@ its root mean square: 2^-21 / sqrt(3) for each of the six, below 2^-19 as well. 
 parts, or parts summed where the whole sum truncates each of them, do not reach it."""
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -200,3 +202,133 @@ def test_replaced_values_under_growth():
         got = binding.gated_delta_rule_step(k[:, t], k[:, t], v[:, t], 2 * one[:, 0], one[:, 0], state, scale=1.0)
         # a value of 1 grows to e^2 and is taken off again: three roundings of e^2 at most
         assert float((got - 1).abs().max()) <= 3 * np.exp(2.0) * 2.0 ** -23
+
+
+def c_bwd(t, do, h0, dh_last, dh0, cu=None):
+    """the C call with dh0 wherever it is told, which the binding always makes itself"""
+    B, L, HK, DK = t["q"].shape
+    H, DV = t["v"].shape[2:]
+    g = {n: torch.empty_like(t[n]) for n in ("q", "k", "v", "g", "beta")}
+    p = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    rc = binding.lib().gated_delta_rule_bwd(
+        *(p(t[n]) for n in ("q", "k", "v", "g", "beta")), p(h0), p(do), p(dh_last),
+        *(p(g[n]) for n in ("q", "k", "v", "g", "beta")), p(dh0), p(cu), B if cu is None else len(cu) - 1, L, HK, H,
+        DK, DV, HK * DK, HK * DK, H * DV, DK ** -0.5, 0, binding._DTYPES[t["q"].dtype], None)
+    torch.cuda.synchronize()
+    assert rc == 0
+    return g
+
+
+# one warp to 16 columns, four warps, many chains, segments; a packed sequence of no tokens
+PLACES = [("bf16", 1, 130, 1, 64, 64, None), ("f32", 1, 130, 1, 64, 48, None), ("f16", 50, 70, 3, 64, 80, None),
+          ("bf16", 1, 2100, 1, 64, 64, None), ("f32", 1, 2100, 1, 32, 16, None),
+          ("bf16", 1, 4500, 1, 32, 16, [0, 2200, 2200, 4500])]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,B,L,H,DK,DV,cu", PLACES)
+def test_states_in_place(dtype, B, L, H, DK, DV, cu):
+    """h_last in h0's place and dh0 in dh_last's: the bits of separate ones"""
+    t, _ = td.dev(td.make(B, L, H, H, DK, DV, decay=0.2), dtype)
+    cut = None if cu is None else torch.tensor(cu, dtype=torch.int32).cuda()
+    n = B if cu is None else len(cu) - 1
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    h0, dh = (torch.randn(n, H, DK, DV, device="cuda", generator=gen) for _ in range(2))
+    o, h = binding.gated_delta_rule_fwd(**t, h0=h0, cu_seqlens=cut, final_state=True)
+    place = h0.clone()
+    o1, h1 = binding.gated_delta_rule_fwd(**t, h0=place, cu_seqlens=cut, h_last=place)
+    assert torch.equal(o, o1) and torch.equal(h, h1) and h1 is place
+    do, apart, place = torch.ones_like(t["v"]), torch.empty_like(dh), dh.clone()
+    g, g1 = c_bwd(t, do, h0, dh, apart, cut), c_bwd(t, do, h0, place, place, cut)
+    assert torch.equal(apart, place) and all(torch.equal(g[m], g1[m]) for m in g)
+    same = binding.gated_delta_rule_bwd(**t, do=do, h0=h0, dh_last=dh, cu_seqlens=cut)
+    assert torch.equal(apart, same["dh0"]) and torch.equal(g["q"], same["dq"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [2, 5])   # token by token, by groups
+def test_more_sequences_than_a_grid_is_deep(L):
+    B, last = 70000, 500
+    gen = torch.Generator(device="cuda").manual_seed(L)
+    rn = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    t = dict(q=rn(B, L, 1, 16).bfloat16(), k=(rn(B, L, 1, 16) / 4).bfloat16(), v=rn(B, L, 1, 16).bfloat16(),
+             g=-rn(B, L, 1).abs(), beta=torch.sigmoid(rn(B, L, 1)))
+    do, h0 = torch.ones_like(t["v"]), rn(B, 1, 16, 16)
+    end = {n: v[-last:].contiguous() for n, v in t.items()}
+    o, h = binding.gated_delta_rule_fwd(**t, h0=h0, final_state=True)
+    o1, h1 = binding.gated_delta_rule_fwd(**end, h0=h0[-last:].contiguous(), final_state=True)
+    assert torch.equal(o[-last:], o1) and torch.equal(h[-last:], h1)
+    g = binding.gated_delta_rule_bwd(**t, do=do, h0=h0, dh_last=h0)
+    g1 = binding.gated_delta_rule_bwd(**end, do=do[-last:], h0=h0[-last:].contiguous(), dh_last=h0[-last:].contiguous())
+    assert all(torch.equal(g[n][-last:], g1[n]) for n in g)
+    if L == 2:
+        one = {n: v[:, 0].contiguous() for n, v in t.items()}
+        slots = torch.arange(B, dtype=torch.int32, device="cuda").flip(0).contiguous()
+        slots[-1] = slots[0]   # the last row's slot has been taken by the first
+        pool = h0.clone()
+        o2 = binding.gated_delta_rule_step(**one, state=pool, slots=slots)
+        some = h0[-last:].contiguous()
+        o3 = binding.gated_delta_rule_step(**{n: v[:last].contiguous() for n, v in one.items()}, state=some,
+                                           slots=(slots[:last] - (B - last)).contiguous())
+        assert torch.equal(o2[:last], o3) and torch.equal(pool[-last:], some)
+        assert not o2[-1].any() and torch.equal(pool[0], h0[0])
+
+
+@pytest.mark.gpu
+def test_calls_from_several_threads():
+    """four threads with a stream each, different shapes at once: the bits of calls one by one"""
+    cases = [td.dev(td.make(1, L, 1, 2, 64, 64, seed=L), d)[0] for L, d in ((300, "bf16"), (130, "f32"), (2200, "bf16"),
+                                                                          (90, "f16"))]
+
+    def call(t):
+        x = t["v"].flatten(0, 1)
+        o, h = binding.gated_delta_rule_fwd(**t, final_state=True)
+        n, _ = binding.block_norm_fwd(o, z=t["v"], post="rms")
+        gn = binding.block_norm_bwd(x, x, post="layer", w_post=torch.ones(64, device="cuda"))
+        return [o, h, n, gn["dx"], gn["dw_post"], *binding.gated_delta_rule_bwd(**t, do=n).values()]
+
+    want = [call(t) for t in cases]
+    torch.cuda.synchronize()
+    got = [None] * len(cases)
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                got[i] = call(cases[i])
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    for w, g in zip(want, got):
+        assert g is not None and all(a is None or torch.equal(a, b) for a, b in zip(w, g))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,L", [("bf16", 200), ("f16", 200), ("f32", 200), ("bf16", 2100), ("f32", 2100)])
+@pytest.mark.parametrize("what", ["v", "k", "g", "beta"])
+def test_what_is_not_finite_stays_where_it_is(dtype, L, what):
+    """in one head of one sequence, from its group of 64 tokens on; its value column in v"""
+    t, _ = td.dev(td.make(1, 3 * L, 2, 2, 32, 32, decay=0.2), dtype)
+    cu = torch.tensor([0, L, 2 * L, 3 * L], dtype=torch.int32).cuda()
+    clean, hc = binding.gated_delta_rule_fwd(**t, cu_seqlens=cu, final_state=True)
+    do = torch.ones_like(clean)
+    gc = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu)
+    t = {n: v.clone() for n, v in t.items()}
+    at = L + 150
+    t[what][(0, at, 1) + ((3,) if what in "vk" else ())] = float("nan")
+    o, h = binding.gated_delta_rule_fwd(**t, cu_seqlens=cu, final_state=True)
+    g = binding.gated_delta_rule_bwd(**t, do=do, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[0, L + 128:2 * L, 1, slice(3, 4) if what == "v" else slice(None)] = False
+    assert torch.equal(o[keep], clean[keep]) and torch.isnan(o[0, at, 1]).any()
+    assert torch.equal(h[[0, 2]], hc[[0, 2]]) and torch.equal(h[1, 0], hc[1, 0]) and torch.isnan(h[1, 1]).any()
+    for n, v in g.items():
+        if v is not None:
+            assert torch.equal(v[:, :L], gc[n][:, :L]) and torch.equal(v[:, 2 * L:], gc[n][:, 2 * L:]), n
+            assert torch.equal(v[:, :, 0], gc[n][:, :, 0]), n
+            assert torch.isnan(v[0, L:at, 1]).any() or n == "dv" or what != "v", n
