@@ -413,7 +413,8 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * NULL = not wanted; h_last may be h0, otherwise no output may overlap an input.  A
  * sequence of no tokens gets h_last = h0.
  * All pointers DEVICE pointers of the current device (SS2D_ERR_PTR otherwise),
- * 16-byte aligned.  Asynchronous on `stream`.  Scratch comes from the stream-ordered
+ * 16-byte aligned but for those read or written value by value (g, beta, dg, dbeta,
+ * cu_seqlens, slots: 4 bytes).  Asynchronous on `stream`.  Scratch comes from the stream-ordered
  * pool, with DKP = 64 or 128, DK rounded up: per group of 64 tokens (ceil(L / 64) to a
  * sequence; packed, L / 64 in all and one more for every sequence, also one of no tokens) and
  * head 21 to 32 KB; for float32 inputs also 768 DKP bytes per group and key head, for few
@@ -426,7 +427,8 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * float32 accuracy, the latter relative to the largest value of a state's column);
  * o is rounded once, on store.  Where o is 16 bits and no h_last is asked for,
  * intermediate values keep 16 bits of mantissa.  A value that is not finite
- * may reach every output of its sequence from its group of 64 tokens on. */
+ * may reach every output of its sequence from its group of 64 tokens on, in the backward
+ * pass every gradient of its sequence. */
 int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const float *g,
                          const float *beta, const float *h0, void *o, float *h_last,
                          const int *cu_seqlens, int nseq, int L, int HK, int H, int DK, int DV,

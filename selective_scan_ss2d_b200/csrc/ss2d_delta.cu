@@ -45,15 +45,17 @@ int validate(const Call &c)
     return SS2D_OK;
 }
 
-// every pointer of `need` is given; those and `opt` are aligned device memory; token strides keep rows aligned
-int check(const Call &c, const void *const *need, int nneed, const void *const *opt, int nopt)
+// Every pointer of `need` is given; those and `opt` are aligned device memory; token strides keep rows aligned.
+// Bit i of `words`: pointer i, of need and then opt, is read or written value by value and may start at any of them
+// (g of one token out of a sequence's)
+int check(const Call &c, const void *const *need, int nneed, const void *const *opt, int nopt, unsigned words)
 {
     const int esz = c.dtype == SS2D_F32 ? 4 : 2;
     for (int i = 0; i < nneed; ++i)
         if (!need[i])
             return SS2D_ERR_NULL;
     for (int i = 0; i < nneed + nopt; ++i)
-        if (((uintptr_t)(i < nneed ? need[i] : opt[i - nneed]) & 15u) != 0)
+        if (((uintptr_t)(i < nneed ? need[i] : opt[i - nneed]) & (words >> i & 1 ? 3u : 15u)) != 0)
             return SS2D_ERR_ALIGN;
     if (c.p.qs * esz % 16 != 0 || c.p.ks * esz % 16 != 0 || c.p.vs * esz % 16 != 0)
         return SS2D_ERR_ALIGN;
@@ -205,9 +207,10 @@ int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const floa
     int rc = validate(c);
     if (rc != SS2D_OK || nseq == 0 || H == 0 || (p.T == 0 && !h_last))
         return rc;
-    const void *opt[] = {h0, h_last, cu_seqlens, q, k, v, g, beta, o};
+    const void *opt[] = {h0, h_last, cu_seqlens};
     const void *need[] = {q, k, v, g, beta, o};
-    rc = p.T ? check(c, need, 6, opt, 3) : check(c, nullptr, 0, opt, 3);
+    const unsigned words = 1 << 3 | 1 << 4 | 1 << 8;   // g, beta, cu_seqlens
+    rc = p.T ? check(c, need, 6, opt, 3, words) : check(c, nullptr, 0, opt, 3, words >> 6);
     if (rc != SS2D_OK)
         return rc;
     if (L <= kRecurLen)
@@ -259,7 +262,8 @@ int gated_delta_rule_bwd(const void *q, const void *k, const void *v, const floa
         return rc;
     const void *opt[] = {h0, dh_last, dh0, cu_seqlens};
     const void *need[] = {q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
-    rc = p.T ? check(c, need, 11, opt, 4) : check(c, nullptr, 0, opt, 4);
+    const unsigned words = 1 << 3 | 1 << 4 | 1 << 9 | 1 << 10 | 1 << 14;   // g, beta, dg, dbeta, cu_seqlens
+    rc = p.T ? check(c, need, 11, opt, 4, words) : check(c, nullptr, 0, opt, 4, words >> 11);
     if (rc != SS2D_OK)
         return rc;
     if (p.T == 0) {   // no token anywhere: the state passes through
@@ -316,7 +320,7 @@ int gated_delta_rule_step(const void *q, const void *k, const void *v, const flo
         return SS2D_OK;
     // a pool of no states: every slot is skipped, the pointer is not read
     const void *need[] = {q, k, v, g, beta, o, nstates ? state : o};
-    rc = check(c, need, 7, reinterpret_cast<const void *const *>(&slots), 1);
+    rc = check(c, need, 7, reinterpret_cast<const void *const *>(&slots), 1, 1 << 3 | 1 << 4 | 1 << 7);   // g, beta, slots
     if (rc != SS2D_OK)
         return rc;
     if (!p.pool)

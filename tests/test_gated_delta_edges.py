@@ -12,6 +12,7 @@ its root mean square: 2^-21 / sqrt(3) for each of the six, below 2^-19 as well. 
 parts, or parts summed where the whole sum truncates each of them, do not reach it."""
 from __future__ import annotations
 
+import ctypes
 import threading
 
 import numpy as np
@@ -33,6 +34,51 @@ def test_backward_without_value_heads_is_refused(lib):
     assert td._bwd(lib, p, HK=1, H=0, vs=0) == -14
     assert td._bwd(lib, p, HK=0, H=0, qs=0, ks=0, vs=0) == 0
     assert td._fwd(lib, p, HK=1, H=0, vs=0) == 0   # an output of no heads
+
+
+def test_alignment_of_values_read_one_by_one(lib):
+    """g, beta, positions and slots may start at any value; half of one is refused"""
+    keep, p = td.ptr()
+    at = lambda n: ctypes.c_void_p(p.value + n)  # noqa: E731
+    head = (1, 8, 1, 2, 16, 16, 16, 16, 32, 1.0)
+    for off, want in ((4, -9), (2, -6)):   # host memory, once the alignment is in order
+        for i in (3, 4, 8):
+            a = [p, p, p, p, p, None, p, None, None]
+            a[i] = at(off)
+            assert lib.gated_delta_rule_fwd(*a, *head, 0, 1, None) in ((want, -8) if want == -9 else (want,)), (off, i)
+        for i in (3, 4, 11, 12, 14):
+            a = [p] * 5 + [None, p, None] + [p] * 5 + [None, None]
+            a[i] = at(off)
+            assert lib.gated_delta_rule_bwd(*a, *head, 0, 1, None) in ((want, -8) if want == -9 else (want,)), (off, i)
+        for i in (3, 4, 6):
+            a = [p] * 6 + [None, p]
+            a[i] = at(off)
+            assert lib.gated_delta_rule_step(*a, 1, 8, *head[2:], 1, None) in ((want, -8) if want == -9 else (want,)), (off, i)
+    for i in (0, 1, 2, 6):
+        a = [p, p, p, p, p, None, p, None, None]
+        a[i] = at(4)
+        assert lib.gated_delta_rule_fwd(*a, *head, 0, 1, None) == -6, i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [1, 3])
+def test_tokens_of_one_sequence_one_by_one(H):
+    """g[:, t] and beta[:, t] of a batch of one, as they lie in the sequence's tensors"""
+    t, _ = td.dev(td.make(1, 9, 1, H, 32, 16), "bf16")
+    pool = torch.zeros(2, 1, H, 32, 16, device="cuda")
+    for i in range(9):
+        row = {n: v[:, i] for n, v in t.items()}
+        o = binding.gated_delta_rule_step(**row, state=pool[0])
+        o1 = binding.gated_delta_rule_step(**{n: v.clone() for n, v in row.items()}, state=pool[1])
+        assert torch.equal(o, o1)
+    assert torch.equal(pool[0], pool[1]) and pool.any()
+    far = {n: torch.cat([v[:, :1], v], 1)[:, 1:] for n, v in t.items()}   # from the second row of a batch of one on
+    cu = torch.tensor([9, 0, 4, 9], dtype=torch.int32).cuda()[1:]
+    do = torch.ones_like(t["v"])
+    for fn, kw in ((binding.gated_delta_rule_fwd, {}), (binding.gated_delta_rule_bwd, dict(do=do))):
+        a, b = fn(**far, **kw, cu_seqlens=cu), fn(**t, **kw, cu_seqlens=cu.clone())
+        a, b = (x.values() if isinstance(x, dict) else x for x in (a, b))
+        assert all(x is None or torch.equal(x, y) for x, y in zip(a, b))
 
 
 @pytest.mark.gpu
