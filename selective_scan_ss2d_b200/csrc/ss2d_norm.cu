@@ -73,10 +73,11 @@ int check(const void *const *need, int nneed, const void *const *opt, int nopt, 
 // Vectors where every row of every tensor starts on a 16-byte boundary, single
 // values otherwise; E values a thread, in teams of the smallest power of two that
 // holds a row.  Rows that fill their teams, of 8 * 2^k values or 12 * 2^k (a width of 192
-// in teams of 16, not of 32 with a quarter idle), have kernels for the combinations
-// that blocks are made of: a norm with or without its gate, a residual, alone or
-// scaled and with biases, with the next norm, all of a block; the others look up what
-// they have.
+// in teams of 16, not of 32 with a quarter idle), have kernels for five combinations of
+// parts: a norm with or without its gate, a residual, alone or scaled and with
+// biases, with the next norm, everything without biases.  The others look up what they
+// have (a layer norm of 25088 rows of 192 with its bias 14.3 us against 10.2 without, backward
+// 41 against 27; every part of 12544 rows of 1024 55 against 45, backward 125 against 80).
 ss2d::NormPlan norm_plan(NormCall &c, bool bwd)
 {
     using namespace ss2d;
