@@ -426,7 +426,9 @@ int ss2d_front_project(const void *x, const float *conv_w, const float *conv_b,
  * cores of operands split into bfloat16 or scaled float16 parts that hold them to
  * float32 accuracy, the latter relative to the largest value of a state's column);
  * o is rounded once, on store.  Where o is 16 bits and no h_last is asked for,
- * intermediate values keep 16 bits of mantissa.  A value that is not finite
+ * intermediate values keep 16 bits of mantissa, and so do in any case the products that
+ * only results stored in 16 bits are made of (q.k inside a group in o, the last ones in
+ * dq and dk).  A value that is not finite
  * may reach every output of its sequence from its group of 64 tokens on, in the backward
  * pass every gradient of its sequence. */
 int gated_delta_rule_fwd(const void *q, const void *k, const void *v, const float *g,
